@@ -16,7 +16,8 @@ from . import build as _build
 FFPA_F16, FFPA_BF16, FFPA_F32 = 0, 1, 2
 STATUS = {0: "FFPA_OK", 1: "FFPA_ERR_INVALID_ARG", 2: "FFPA_ERR_UNSUPPORTED", 3: "FFPA_ERR_ALIGNMENT",
           4: "FFPA_ERR_CUDA", 5: "FFPA_ERR_TIMEOUT", 6: "FFPA_ERR_SCRATCH_LIMIT"}
-EXPORTS = ("ffpa_fwd", "ffpa_bwd", "ffpa_fwd_dropout", "ffpa_bwd_dropout", "ffpa_fwd_decode_noalloc", "ffpa_status_string", "ffpa_check_status",
+EXPORTS = ("ffpa_fwd", "ffpa_bwd", "ffpa_fwd_dropout", "ffpa_bwd_dropout", "ffpa_fwd_decode_noalloc",
+           "ffpa_fwd_varlen", "ffpa_bwd_varlen", "ffpa_status_string", "ffpa_check_status",
            "ffpa_set_timing_events", "ffpa_selftest_wait_timeout", "ffpa_version")
 
 
@@ -56,6 +57,11 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.ffpa_bwd_dropout.restype = ctypes.c_int
     lib.ffpa_fwd_decode_noalloc.argtypes = [P, P, P, P, ctypes.c_int, ctypes.c_float, P, P, ctypes.c_void_p]
     lib.ffpa_fwd_decode_noalloc.restype = ctypes.c_int
+    I, F, V = ctypes.c_int, ctypes.c_float, ctypes.c_void_p
+    lib.ffpa_fwd_varlen.argtypes = [P, P, P, V, I, I, F, P, P, V]
+    lib.ffpa_fwd_varlen.restype = I
+    lib.ffpa_bwd_varlen.argtypes = [P, P, P, V, I, I, F, P, P, P, P, P, P, V]
+    lib.ffpa_bwd_varlen.restype = I
     lib.ffpa_status_string.argtypes = [ctypes.c_int]
     lib.ffpa_status_string.restype = ctypes.c_char_p
     lib.ffpa_check_status.argtypes = [ctypes.c_void_p]
@@ -184,6 +190,37 @@ def ffpa_bwd(q, k, v, bias, causal, scale, out, lse, dout, dq, dk, dv, stream=No
         [describe(x) for x in (dout, dq, dk, dv)]
     rc = lib.ffpa_bwd(*[_ref(x) for x in ds[:4]], int(causal), float(scale), *[_ref(x) for x in ds[4:]],
                       _stream(stream))
+    _raise(rc)
+
+
+def _ints(t, name, dims, dtype="int32"):
+    """Device address of a contiguous integer (or bool) tensor of `dims` dimensions."""
+    import torch
+    if t.dtype != getattr(torch, dtype) or t.dim() != dims or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {dims} dimension(s), "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def ffpa_fwd_varlen(q, k, v, cu_seqlens, causal, scale, out, lse, stream=None) -> None:
+    """Call ffpa_fwd_varlen (the forward over packed sequences); raises FfpaError on a non-zero status."""
+    lib = load()
+    cu = _ints(cu_seqlens, "cu_seqlens", 1)
+    check_devices((q, k, v, cu_seqlens, out, lse), _current_device())
+    ds = [describe(q), describe(k), describe(v), describe(out), describe(lse, as_lse=True)]
+    rc = lib.ffpa_fwd_varlen(*[_ref(x) for x in ds[:3]], cu, cu_seqlens.shape[0] - 1, int(causal), float(scale),
+                             _ref(ds[3]), _ref(ds[4]), _stream(stream))
+    _raise(rc)
+
+
+def ffpa_bwd_varlen(q, k, v, cu_seqlens, causal, scale, out, lse, dout, dq, dk, dv, stream=None) -> None:
+    """Call ffpa_bwd_varlen (the backward of ffpa_fwd_varlen); raises FfpaError on a non-zero status."""
+    lib = load()
+    cu = _ints(cu_seqlens, "cu_seqlens", 1)
+    check_devices((q, k, v, cu_seqlens, out, lse, dout, dq, dk, dv), _current_device())
+    ds = [describe(x) for x in (q, k, v, out)] + [describe(lse, as_lse=True)] + [describe(x) for x in (dout, dq, dk, dv)]
+    rc = lib.ffpa_bwd_varlen(*[_ref(x) for x in ds[:3]], cu, cu_seqlens.shape[0] - 1, int(causal), float(scale),
+                             *[_ref(x) for x in ds[3:]], _stream(stream))
     _raise(rc)
 
 

@@ -287,6 +287,91 @@ int drop_params(const DropArgs* d, int* on, uint32_t* t, uint32_t* seed_lo, uint
   return FFPA_OK;
 }
 
+// The kernels' parameters of a forward, without dropout, key splits or packing.
+void fill_fwd(FwdParams* out_p, const Common& c, const ffpa_tensor_t* q, const ffpa_tensor_t* bias, int causal,
+              float scale, const ffpa_tensor_t* out, const ffpa_tensor_t* lse, uint32_t* status) {
+  FwdParams p = {};
+  int64_t bsb, bsh, bsq, bsk;
+  bias_strides(bias, &bsb, &bsh, &bsq, &bsk);
+  p.out = out->data;
+  p.lse = lse ? static_cast<float*>(lse->data) : nullptr;
+  p.bias = bias ? static_cast<const float*>(bias->data) : nullptr;
+  p.q = q->data;
+  p.q_sb = q->stride[0]; p.q_sh = q->stride[1]; p.q_sn = q->stride[2];
+  p.o_sb = out->stride[0]; p.o_sh = out->stride[1]; p.o_sn = out->stride[2];
+  p.bias_sb = bsb; p.bias_sh = bsh; p.bias_sq = bsq; p.bias_sk = bsk;
+  p.bias_vec = bias && bsk == 1 && reinterpret_cast<uintptr_t>(bias->data) % 16 == 0 && bsb % 4 == 0 &&
+               bsh % 4 == 0 && bsq % 4 == 0;
+  p.B = (int)c.B; p.Hq = (int)c.Hq; p.Hkv = (int)c.Hkv; p.Nq = (int)c.Nq; p.Nkv = (int)c.Nkv; p.D = (int)c.D;
+  p.group = (int)(c.Hq / c.Hkv);
+  p.causal = causal;
+  p.scale_log2 = scale * kLog2e;
+  p.n_chunks = (int)(c.D / kChunk);
+  p.q_tiles = (int)((c.Nq + kTileRows - 1) / kTileRows);
+  p.status = status;
+  p.drop_scale = 1.f;
+  *out_p = p;
+}
+
+int encode_fwd_maps(FwdMaps* m, const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_tensor_t* v) {
+  int rc;
+  if ((rc = encode_map(&m->q, q)) || (rc = encode_map(&m->k, k)) || (rc = encode_map(&m->v, v)) ||
+      (rc = encode_map(&m->k_half, k, kTileRows / 2)) || (rc = encode_map(&m->q_half, q, kTileRows / 2)))
+    return rc;
+  return FFPA_OK;
+}
+
+// The kernels' parameters of a backward, without dropout or packing.
+void fill_bwd(BwdParams* out_p, const Common& c, const ffpa_tensor_t* q, const ffpa_tensor_t* k,
+              const ffpa_tensor_t* v, const ffpa_tensor_t* bias, int causal, float scale, const ffpa_tensor_t* out,
+              const ffpa_tensor_t* lse, const ffpa_tensor_t* dout, const ffpa_tensor_t* dq, const ffpa_tensor_t* dk,
+              const ffpa_tensor_t* dv, uint32_t* status) {
+  int64_t bsb, bsh, bsq, bsk;
+  bias_strides(bias, &bsb, &bsh, &bsq, &bsk);
+  BwdParams p = {};
+  p.out = out->data;
+  p.dout = dout->data;
+  p.lse = static_cast<const float*>(lse->data);
+  p.bias = bias ? static_cast<const float*>(bias->data) : nullptr;
+  p.dq = dq->data;
+  p.dk = dk->data;
+  p.dv = dv->data;
+  p.q = q->data;
+  p.k = k->data;
+  p.v = v->data;
+  p.q_sb = q->stride[0]; p.q_sh = q->stride[1]; p.q_sn = q->stride[2];
+  p.k_sb = k->stride[0]; p.k_sh = k->stride[1]; p.k_sn = k->stride[2];
+  p.v_sb = v->stride[0]; p.v_sh = v->stride[1]; p.v_sn = v->stride[2];
+  p.o_sb = out->stride[0]; p.o_sh = out->stride[1]; p.o_sn = out->stride[2];
+  p.do_sb = dout->stride[0]; p.do_sh = dout->stride[1]; p.do_sn = dout->stride[2];
+  p.dq_sb = dq->stride[0]; p.dq_sh = dq->stride[1]; p.dq_sn = dq->stride[2];
+  p.dk_sb = dk->stride[0]; p.dk_sh = dk->stride[1]; p.dk_sn = dk->stride[2];
+  p.dv_sb = dv->stride[0]; p.dv_sh = dv->stride[1]; p.dv_sn = dv->stride[2];
+  p.bias_sb = bsb; p.bias_sh = bsh; p.bias_sq = bsq; p.bias_sk = bsk;
+  p.B = (int)c.B; p.Hq = (int)c.Hq; p.Hkv = (int)c.Hkv; p.Nq = (int)c.Nq; p.Nkv = (int)c.Nkv; p.D = (int)c.D;
+  p.group = (int)(c.Hq / c.Hkv);
+  p.causal = causal;
+  p.scale = scale;
+  p.scale_log2 = scale * kLog2e;
+  p.n_chunks = (int)(c.D / kChunk);
+  p.q_tiles = (int)((c.Nq + kTileRows - 1) / kTileRows);
+  p.kv_tiles = (int)((c.Nkv + kTileRows - 1) / kTileRows);
+  p.status = status;
+  p.drop_scale = 1.f;
+  *out_p = p;
+}
+
+int encode_bwd_maps(BwdMaps* m, const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_tensor_t* v,
+                    const ffpa_tensor_t* dout) {
+  int rc;
+  if ((rc = encode_map(&m->q, q)) || (rc = encode_map(&m->k, k)) || (rc = encode_map(&m->v, v)) ||
+      (rc = encode_map(&m->dout, dout)) || (rc = encode_map(&m->q_half, q, kTileRows / 2)) ||
+      (rc = encode_map(&m->k_half, k, kTileRows / 2)) || (rc = encode_map(&m->v_half, v, kTileRows / 2)) ||
+      (rc = encode_map(&m->dout_half, dout, kTileRows / 2)))
+    return rc;
+  return FFPA_OK;
+}
+
 int fwd_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_tensor_t* v, const ffpa_tensor_t* bias,
              int causal, float scale, const DropArgs* drop, const ffpa_tensor_t* out, const ffpa_tensor_t* lse,
              ffpa_stream_t stream) {
@@ -342,30 +427,13 @@ int fwd_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_tensor_t
     return cuda_rc(e != cudaSuccess ? e : e2);
   }
 
-  FwdParams p = {};
-  p.out = out->data;
-  p.lse = lse ? static_cast<float*>(lse->data) : nullptr;
-  p.bias = bias ? static_cast<const float*>(bias->data) : nullptr;
-  p.q = q->data;
-  p.q_sb = q->stride[0]; p.q_sh = q->stride[1]; p.q_sn = q->stride[2];
-  p.o_sb = out->stride[0]; p.o_sh = out->stride[1]; p.o_sn = out->stride[2];
-  p.bias_sb = bsb; p.bias_sh = bsh; p.bias_sq = bsq; p.bias_sk = bsk;
-  p.bias_vec = bias && bsk == 1 && reinterpret_cast<uintptr_t>(bias->data) % 16 == 0 && bsb % 4 == 0 &&
-               bsh % 4 == 0 && bsq % 4 == 0;
-  p.B = (int)c.B; p.Hq = (int)c.Hq; p.Hkv = (int)c.Hkv; p.Nq = (int)c.Nq; p.Nkv = (int)c.Nkv; p.D = (int)c.D;
-  p.group = (int)(c.Hq / c.Hkv);
-  p.causal = causal;
-  p.scale_log2 = scale * kLog2e;
-  p.n_chunks = (int)(c.D / kChunk);
-  p.q_tiles = (int)((c.Nq + kTileRows - 1) / kTileRows);
-  p.status = status;
+  FwdParams p;
+  fill_fwd(&p, c, q, bias, causal, scale, out, lse, status);
   p.dropout = dropout;
   p.drop_t = drop_t; p.drop_seed_lo = seed_lo; p.drop_seed_hi = seed_hi; p.drop_off = drop_off;
   p.drop_scale = drop_scale;
   FwdMaps m;
-  if ((rc = encode_map(&m.q, q)) || (rc = encode_map(&m.k, k)) || (rc = encode_map(&m.v, v)) ||
-      (rc = encode_map(&m.k_half, k, kTileRows / 2)) || (rc = encode_map(&m.q_half, q, kTileRows / 2)))
-    return rc;
+  if ((rc = encode_fwd_maps(&m, q, k, v))) return rc;
   int per = 0;
   const int splits = fwd_fulld_supported(p) ? fwd_fulld_kv_splits(p, device_sm_count(), &per) : 1;
   if (splits > 1) {
@@ -420,46 +488,13 @@ int bwd_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_tensor_t
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint32_t* status = device_status_word();
   if (!status) return FFPA_ERR_CUDA;
-  int64_t bsb, bsh, bsq, bsk;
-  bias_strides(bias, &bsb, &bsh, &bsq, &bsk);
-  BwdParams p = {};
-  p.out = out->data;
-  p.dout = dout->data;
-  p.lse = static_cast<const float*>(lse->data);
-  p.bias = bias ? static_cast<const float*>(bias->data) : nullptr;
-  p.dq = dq->data;
-  p.dk = dk->data;
-  p.dv = dv->data;
-  p.q = q->data;
-  p.k = k->data;
-  p.v = v->data;
-  p.q_sb = q->stride[0]; p.q_sh = q->stride[1]; p.q_sn = q->stride[2];
-  p.k_sb = k->stride[0]; p.k_sh = k->stride[1]; p.k_sn = k->stride[2];
-  p.v_sb = v->stride[0]; p.v_sh = v->stride[1]; p.v_sn = v->stride[2];
-  p.o_sb = out->stride[0]; p.o_sh = out->stride[1]; p.o_sn = out->stride[2];
-  p.do_sb = dout->stride[0]; p.do_sh = dout->stride[1]; p.do_sn = dout->stride[2];
-  p.dq_sb = dq->stride[0]; p.dq_sh = dq->stride[1]; p.dq_sn = dq->stride[2];
-  p.dk_sb = dk->stride[0]; p.dk_sh = dk->stride[1]; p.dk_sn = dk->stride[2];
-  p.dv_sb = dv->stride[0]; p.dv_sh = dv->stride[1]; p.dv_sn = dv->stride[2];
-  p.bias_sb = bsb; p.bias_sh = bsh; p.bias_sq = bsq; p.bias_sk = bsk;
-  p.B = (int)c.B; p.Hq = (int)c.Hq; p.Hkv = (int)c.Hkv; p.Nq = (int)c.Nq; p.Nkv = (int)c.Nkv; p.D = (int)c.D;
-  p.group = (int)(c.Hq / c.Hkv);
-  p.causal = causal;
-  p.scale = scale;
-  p.scale_log2 = scale * kLog2e;
-  p.n_chunks = (int)(c.D / kChunk);
-  p.q_tiles = (int)((c.Nq + kTileRows - 1) / kTileRows);
-  p.kv_tiles = (int)((c.Nkv + kTileRows - 1) / kTileRows);
-  p.status = status;
+  BwdParams p;
+  fill_bwd(&p, c, q, k, v, bias, causal, scale, out, lse, dout, dq, dk, dv, status);
   p.dropout = dropout;
   p.drop_t = drop_t; p.drop_seed_lo = seed_lo; p.drop_seed_hi = seed_hi; p.drop_off = drop_off;
   p.drop_scale = drop_scale;
   BwdMaps m;
-  if ((rc = encode_map(&m.q, q)) || (rc = encode_map(&m.k, k)) || (rc = encode_map(&m.v, v)) ||
-      (rc = encode_map(&m.dout, dout)) || (rc = encode_map(&m.q_half, q, kTileRows / 2)) ||
-      (rc = encode_map(&m.k_half, k, kTileRows / 2)) || (rc = encode_map(&m.v_half, v, kTileRows / 2)) ||
-      (rc = encode_map(&m.dout_half, dout, kTileRows / 2)))
-    return rc;
+  if ((rc = encode_bwd_maps(&m, q, k, v, dout))) return rc;
   const size_t rows = (size_t)c.B * c.Hq * c.Nq;
   timing_begin();
   void* scratch = nullptr;
@@ -467,6 +502,142 @@ int bwd_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_tensor_t
   p.delta = static_cast<float*>(scratch);
   p.lse2 = p.delta + rows;
   cudaError_t e = launch_bwd(p, m, dtype_is_bf16(c.dtype), st);
+  cudaError_t e2 = cudaFreeAsync(scratch, st);
+  return cuda_rc(e != cudaSuccess ? e : e2);
+}
+
+// ------------------------------------------------------------ packed sequences
+// Checks beyond check_common: one batch, as many keys as queries, and the starts.
+int check_packed(const Common& c, const int32_t* cu_seqlens, int n_seqs, int causal) {
+  if (c.B != 1 || c.Nq != c.Nkv) return FFPA_ERR_INVALID_ARG;
+  if (!cu_seqlens || n_seqs < 1 || (causal != 0 && causal != 1)) return FFPA_ERR_INVALID_ARG;
+  if (n_seqs > (1 << 20)) return FFPA_ERR_UNSUPPORTED;
+  if (reinterpret_cast<uintptr_t>(cu_seqlens) % 4 != 0) return FFPA_ERR_ALIGNMENT;
+  return FFPA_OK;
+}
+
+size_t round_up(size_t x, size_t to) { return (x + to - 1) / to * to; }
+
+// The plan of a packed call in `scratch` (bytes from var_scratch_bytes, 128-byte aligned).
+struct VarLayout {
+  int slots;
+  size_t maps_bytes, bytes;
+};
+VarLayout var_layout(int64_t T, int n_seqs) {
+  VarLayout l;
+  // sum over the sequences of ceil(len / 128) is at most (T + 127 n) / 128, and at most T
+  l.slots = static_cast<int>(std::min<int64_t>((T + int64_t(kTileRows - 1) * n_seqs) / kTileRows, T));
+  l.maps_bytes = static_cast<size_t>(n_seqs) * kVarMaps * sizeof(CUtensorMap);
+  l.bytes = round_up(l.maps_bytes + static_cast<size_t>(l.slots) * sizeof(int4), 128);
+  return l;
+}
+
+void fill_plan(VarPlan* plan, VarParams* var, const VarLayout& l, const Common& c, const int32_t* cu, int n_seqs,
+               int causal, char* scratch, uint32_t* status) {
+  var->maps = reinterpret_cast<const CUtensorMap*>(scratch);
+  var->tiles = reinterpret_cast<const int4*>(scratch + l.maps_bytes);
+  var->slots = l.slots;
+  var->total = static_cast<int>(c.Nq);
+  plan->n_maps = 0;
+  plan->cu = cu;
+  plan->n_seqs = n_seqs;
+  plan->total = static_cast<int>(c.Nq);
+  plan->slots = l.slots;
+  plan->causal = causal;
+  plan->bin_shift = 0;
+  while ((c.Nq / kTileRows + 1) >> plan->bin_shift >= 1024) ++plan->bin_shift;
+  plan->out_maps = reinterpret_cast<CUtensorMap*>(scratch);
+  plan->tiles = reinterpret_cast<int4*>(scratch + l.maps_bytes);
+  plan->status = status;
+}
+
+void plan_map(VarPlan* plan, const CUtensorMap& m, const ffpa_tensor_t* t) {
+  int64_t st[3];
+  tma_strides(t, st);
+  plan->maps[plan->n_maps] = m;
+  plan->base[plan->n_maps] = t->data;
+  plan->row_stride[plan->n_maps++] = st[0];
+}
+
+int fwd_varlen_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_tensor_t* v, const int32_t* cu_seqlens,
+                    int n_seqs, int causal, float scale, const ffpa_tensor_t* out, const ffpa_tensor_t* lse,
+                    ffpa_stream_t stream) {
+  Common c;
+  int rc = check_common(q, k, v, nullptr, scale, &c);
+  if (rc) return rc;
+  if ((rc = check_packed(c, cu_seqlens, n_seqs, causal))) return rc;
+  if ((rc = check_bhnd(out, c.dtype, {c.B, c.Hq, c.Nq, c.D}))) return rc;
+  if (lse && (rc = check_lse(lse, c))) return rc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint32_t* status = device_status_word();
+  if (!status) return FFPA_ERR_CUDA;
+  FwdParams p;
+  fill_fwd(&p, c, q, nullptr, causal, scale, out, lse, status);
+  FwdMaps m;
+  if ((rc = encode_fwd_maps(&m, q, k, v))) return rc;
+  const VarLayout l = var_layout(c.Nq, n_seqs);
+  timing_begin();
+  void* scratch = nullptr;
+  if (scratch_alloc(&scratch, l.bytes, st) != cudaSuccess) return FFPA_ERR_CUDA;
+  VarPlan plan;
+  fill_plan(&plan, &p.var, l, c, cu_seqlens, n_seqs, causal, static_cast<char*>(scratch), status);
+  const bool pair = c.D >= 320;  // the CTA-pair kernels load halves of the Q and K tiles
+  plan_map(&plan, pair ? m.q_half : m.q, q);
+  plan_map(&plan, pair ? m.k_half : m.k, k);
+  plan_map(&plan, m.v, v);
+  timing_mark(st);
+  cudaError_t e = launch_varlen_plan(plan, st);
+  if (e == cudaSuccess) e = launch_fwd_main(p, m, dtype_is_bf16(c.dtype), st);
+  cudaError_t e2 = cudaFreeAsync(scratch, st);
+  return cuda_rc(e != cudaSuccess ? e : e2);
+}
+
+int bwd_varlen_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_tensor_t* v, const int32_t* cu_seqlens,
+                    int n_seqs, int causal, float scale, const ffpa_tensor_t* out, const ffpa_tensor_t* lse,
+                    const ffpa_tensor_t* dout, const ffpa_tensor_t* dq, const ffpa_tensor_t* dk,
+                    const ffpa_tensor_t* dv, ffpa_stream_t stream) {
+  Common c;
+  int rc = check_common(q, k, v, nullptr, scale, &c);
+  if (rc) return rc;
+  if ((rc = check_packed(c, cu_seqlens, n_seqs, causal))) return rc;
+  if ((rc = check_bhnd(out, c.dtype, {c.B, c.Hq, c.Nq, c.D}))) return rc;
+  if ((rc = check_bhnd(dout, c.dtype, {c.B, c.Hq, c.Nq, c.D}))) return rc;
+  if ((rc = check_bhnd(dq, c.dtype, {c.B, c.Hq, c.Nq, c.D}))) return rc;
+  if ((rc = check_bhnd(dk, c.dtype, {c.B, c.Hkv, c.Nkv, c.D}))) return rc;
+  if ((rc = check_bhnd(dv, c.dtype, {c.B, c.Hkv, c.Nkv, c.D}))) return rc;
+  if (!lse) return FFPA_ERR_INVALID_ARG;
+  if ((rc = check_lse(lse, c))) return rc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint32_t* status = device_status_word();
+  if (!status) return FFPA_ERR_CUDA;
+  BwdParams p;
+  fill_bwd(&p, c, q, k, v, nullptr, causal, scale, out, lse, dout, dq, dk, dv, status);
+  BwdMaps m;
+  if ((rc = encode_bwd_maps(&m, q, k, v, dout))) return rc;
+  const VarLayout l = var_layout(c.Nq, n_seqs);
+  const size_t rows = static_cast<size_t>(c.Hq) * c.Nq;
+  timing_begin();
+  void* scratch = nullptr;
+  if (scratch_alloc(&scratch, l.bytes + rows * 2 * sizeof(float), st) != cudaSuccess) return FFPA_ERR_CUDA;
+  p.delta = reinterpret_cast<float*>(static_cast<char*>(scratch) + l.bytes);
+  p.lse2 = p.delta + rows;
+  VarPlan plan;
+  fill_plan(&plan, &p.var, l, c, cu_seqlens, n_seqs, causal, static_cast<char*>(scratch), status);
+  if (c.D >= 320) {
+    plan_map(&plan, m.q_half, q);
+    plan_map(&plan, m.k_half, k);
+    plan_map(&plan, m.v_half, v);
+    plan_map(&plan, m.dout_half, dout);
+    plan_map(&plan, m.k, k);
+  } else {
+    plan_map(&plan, m.q, q);
+    plan_map(&plan, m.k, k);
+    plan_map(&plan, m.v, v);
+    plan_map(&plan, m.dout, dout);
+  }
+  timing_mark(st);
+  cudaError_t e = launch_varlen_plan(plan, st);
+  if (e == cudaSuccess) e = launch_bwd(p, m, dtype_is_bf16(c.dtype), st);
   cudaError_t e2 = cudaFreeAsync(scratch, st);
   return cuda_rc(e != cudaSuccess ? e : e2);
 }
@@ -501,6 +672,20 @@ extern "C" int ffpa_bwd_dropout(const ffpa_tensor_t* q, const ffpa_tensor_t* k, 
                                 const ffpa_tensor_t* dv, ffpa_stream_t stream) {
   const DropArgs d = {dropout_p, seed, offset};
   return bwd_impl(q, k, v, bias, causal, scale, &d, out, lse, dout, dq, dk, dv, stream);
+}
+
+extern "C" int ffpa_fwd_varlen(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_tensor_t* v,
+                               const int32_t* cu_seqlens, int n_seqs, int causal, float scale,
+                               const ffpa_tensor_t* out, const ffpa_tensor_t* lse, ffpa_stream_t stream) {
+  return fwd_varlen_impl(q, k, v, cu_seqlens, n_seqs, causal, scale, out, lse, stream);
+}
+
+extern "C" int ffpa_bwd_varlen(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_tensor_t* v,
+                               const int32_t* cu_seqlens, int n_seqs, int causal, float scale,
+                               const ffpa_tensor_t* out, const ffpa_tensor_t* lse, const ffpa_tensor_t* dout,
+                               const ffpa_tensor_t* dq, const ffpa_tensor_t* dk, const ffpa_tensor_t* dv,
+                               ffpa_stream_t stream) {
+  return bwd_varlen_impl(q, k, v, cu_seqlens, n_seqs, causal, scale, out, lse, dout, dq, dk, dv, stream);
 }
 
 // Decode without allocation: validation and parameters as ffpa_fwd's decode
@@ -564,7 +749,7 @@ extern "C" int ffpa_check_status(ffpa_stream_t stream) {
   if (v != 0) {
     const uint32_t zero = 0;
     if (cudaMemcpyToSymbol(g_status_word, &zero, sizeof(zero)) != cudaSuccess) return FFPA_ERR_CUDA;
-    return v == FFPA_DEV_TIMEOUT ? FFPA_ERR_TIMEOUT : FFPA_ERR_CUDA;
+    return v == FFPA_DEV_TIMEOUT ? FFPA_ERR_TIMEOUT : v == FFPA_DEV_LENGTHS ? FFPA_ERR_INVALID_ARG : FFPA_ERR_CUDA;
   }
   return FFPA_OK;
 }

@@ -30,6 +30,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "varlen.cuh"
 
 namespace ffpa {
 namespace {
@@ -138,12 +139,12 @@ struct Geo {
   int rot;            // column sweep starts here (stationary tiles start at different columns)
 };
 
-template <int MODE>
-__device__ __forceinline__ Geo make_geo(const BwdParams& p) {
+template <int MODE, bool VAR>
+__device__ __forceinline__ Geo make_geo(const BwdParams& p, const VarTile& vt) {
   Geo g;
   g.b = blockIdx.z;
   if (MODE == kDQ) {
-    const int qt = p.q_tiles - 1 - static_cast<int>(blockIdx.x);  // heavy causal tiles first
+    const int qt = VAR ? vt.tile : p.q_tiles - 1 - static_cast<int>(blockIdx.x);  // heavy causal tiles first
     g.h = blockIdx.y;
     g.kvh = g.h / p.group;
     g.s_head = g.h;
@@ -155,7 +156,9 @@ __device__ __forceinline__ Geo make_geo(const BwdParams& p) {
     g.nq_h = 0;
     g.rot = g.ncols > 0 ? qt % g.ncols : 0;
   } else {
-    const int kvt = static_cast<int>(blockIdx.x);
+    // packed: the slots are in the order of the query tiles' work; key tile
+    // kv_tiles - 1 - t of a causal sequence has the work of query tile t
+    const int kvt = VAR ? p.kv_tiles - 1 - vt.tile : static_cast<int>(blockIdx.x);
     g.kvh = blockIdx.y;
     g.h = g.kvh * p.group;
     g.s_head = g.kvh;
@@ -186,11 +189,21 @@ __device__ __forceinline__ void column(const Geo& g, const BwdParams& p, int c, 
   }
 }
 
-template <int MODE, bool BF16>
+template <int MODE, bool BF16, bool VAR>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_main_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                     const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
-                    const __grid_constant__ BwdParams p, const int n_res) {
+                    const __grid_constant__ BwdParams p_in, const int n_res) {
+  // packed sequences: this block's sequence and tile, and the call's parameters for that sequence
+  VarTile vt = {};
+  BwdParams p_var;
+  if constexpr (VAR) {
+    vt = var_tile(p_in.var, static_cast<int>(blockIdx.x));
+    if (vt.seq < 0) return;  // an empty slot
+    p_var = p_in;
+    localize(p_var, vt);
+  }
+  const BwdParams& p = VAR ? p_var : p_in;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int stages = p.stages;
@@ -205,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t a_sm = s_base + plan.a_off, ring_sm = s_base + plan.ring_off;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const Geo g = make_geo<MODE>(p);
+  const Geo g = make_geo<MODE, VAR>(p, vt);
   const int n = p.n_chunks;
   // the score products reduce over chunks s0 .. s0 + s_n - 1 and the gradient
   // covers chunks own0 .. own0 + own_n - 1: all of D
@@ -214,11 +227,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool two = (MODE != kDV);  // a second score-like product (dP)
   uint32_t* status = p.status;
 
-  const CUtensorMap* mA1 = (MODE == kDQ) ? &map_q : &map_k;
-  const CUtensorMap* mA2 = (MODE == kDQ) ? &map_do : &map_v;
-  const CUtensorMap* mB1 = (MODE == kDQ) ? &map_k : &map_q;
-  const CUtensorMap* mB2 = (MODE == kDQ) ? &map_v : &map_do;
-  const CUtensorMap* mB3 = (MODE == kDV) ? &map_do : ((MODE == kDK) ? &map_q : &map_k);
+  const CUtensorMap* m_q = VAR ? var_map(p.var, vt, 0) : &map_q;
+  const CUtensorMap* m_k = VAR ? var_map(p.var, vt, 1) : &map_k;
+  const CUtensorMap* m_v = VAR ? var_map(p.var, vt, 2) : &map_v;
+  const CUtensorMap* m_do = VAR ? var_map(p.var, vt, 3) : &map_do;
+  const CUtensorMap* mA1 = (MODE == kDQ) ? m_q : m_k;
+  const CUtensorMap* mA2 = (MODE == kDQ) ? m_do : m_v;
+  const CUtensorMap* mB1 = (MODE == kDQ) ? m_k : m_q;
+  const CUtensorMap* mB2 = (MODE == kDQ) ? m_v : m_do;
+  const CUtensorMap* mB3 = (MODE == kDV) ? m_do : ((MODE == kDK) ? m_q : m_k);
 
   if (tid == 0) {
     for (int i = 0; i < stages; ++i) {
@@ -257,10 +274,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nprod = min(kProducers, stages);
     const int pi = (warp == 0) ? 0 : warp - 1;
     if (lane == 0 && pi < nprod) {
-      tma_prefetch_desc(&map_q);
-      tma_prefetch_desc(&map_k);
-      tma_prefetch_desc(&map_v);
-      tma_prefetch_desc(&map_do);
+      if constexpr (VAR) {
+        var_map_acquire(m_q);
+        var_map_acquire(m_k);
+        var_map_acquire(m_v);
+        var_map_acquire(m_do);
+      }
+      tma_prefetch_desc(m_q);
+      tma_prefetch_desc(m_k);
+      tma_prefetch_desc(m_v);
+      tma_prefetch_desc(m_do);
       if (pi == 0 && n_res > 0) {
         mbar_expect_tx(bar(bl.a_full), n_res * s_n * kChunkBytes);
         for (int c = 0; c < s_n; ++c) {
@@ -519,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>((warp - 4) * 32) << 16;
     float lse2_row = 0.f, delta_row = 0.f;
     if (MODE == kDQ) {
-      const int64_t idx = (static_cast<int64_t>(g.b) * p.Hq + g.h) * p.Nq + min(srow, p.Nq - 1);
+      const int64_t idx = (static_cast<int64_t>(g.b) * p.Hq + g.h) * stat_rows<VAR>(p) + min(srow, p.Nq - 1);
       lse2_row = p.lse2[idx];
       delta_row = p.delta[idx];
     }
@@ -546,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // score.  The loads are issued before the wait so their latency hides.
         float l2v[4] = {0.f, 0.f, 0.f, 0.f}, dlv[4] = {0.f, 0.f, 0.f, 0.f};
         if (MODE != kDQ) {
-          const int64_t sbase = (static_cast<int64_t>(g.b) * p.Hq + ch) * p.Nq;
+          const int64_t sbase = (static_cast<int64_t>(g.b) * p.Hq + ch) * stat_rows<VAR>(p);
 #pragma unroll
           for (int c4 = 0; c4 < 4; ++c4) {
             const int64_t i = sbase + min(cr0 + c4 * 32 + lane, p.Nq - 1);
@@ -734,11 +757,12 @@ cudaError_t launch_mode(const BwdParams& p_in, const BwdMaps& m, cudaStream_t st
   p.slot_chunks = G;
   const Plan plan = make_plan(p.n_chunks, stages, n_res, G);
   const int smem = plan.total + 1024;
-  auto kern = bwd_main_kernel<MODE, BF16>;
+  auto kern = p.var.tiles ? bwd_main_kernel<MODE, BF16, true> : bwd_main_kernel<MODE, BF16, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = (MODE == kDQ) ? dim3(p.q_tiles, p.Hq, p.B) : dim3(p.kv_tiles, p.Hkv, p.B);
+  const int slots = p.var.tiles ? p.var.slots : (MODE == kDQ ? p.q_tiles : p.kv_tiles);
+  cfg.gridDim = dim3(slots, MODE == kDQ ? p.Hq : p.Hkv, p.B);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

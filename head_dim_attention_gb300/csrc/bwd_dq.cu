@@ -51,6 +51,7 @@
 #include "internal.h"
 #include "philox.cuh"
 #include "ptx.cuh"
+#include "varlen.cuh"
 
 namespace ffpa {
 namespace {
@@ -111,11 +112,12 @@ struct Geo {
   int rot;        // the key sweep starts here
 };
 
-__device__ __forceinline__ Geo make_geo(const BwdParams& p, int rank) {
+template <bool VAR>
+__device__ __forceinline__ Geo make_geo(const BwdParams& p, const VarTile& vt, int rank) {
   Geo g;
   g.b = blockIdx.z;
   const int pair = static_cast<int>(blockIdx.x) >> 1;
-  g.st = p.q_tiles - 1 - pair;  // heavy causal tiles first
+  g.st = VAR ? vt.tile : p.q_tiles - 1 - pair;  // heavy causal tiles first
   g.h = blockIdx.y;
   g.kvh = g.h / p.group;
   const int kv_end = p.causal ? min(p.Nkv, (g.st + 1) * kTileRows) : p.Nkv;
@@ -132,11 +134,21 @@ __device__ __forceinline__ int column(const Geo& g, int c) {
   return c * kTileRows;
 }
 
-template <int NC, bool BF16, bool DROP>
+template <int NC, bool BF16, bool DROP, bool VAR>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_qh,
                   const __grid_constant__ CUtensorMap map_kh, const __grid_constant__ CUtensorMap map_vh,
-                  const __grid_constant__ CUtensorMap map_doh, const __grid_constant__ BwdParams p) {
+                  const __grid_constant__ CUtensorMap map_doh, const __grid_constant__ BwdParams p_in) {
+  // packed sequences: this pair's sequence and tile, and the call's parameters for that sequence
+  VarTile vt = {};
+  BwdParams p_var;
+  if constexpr (VAR) {
+    vt = var_tile(p_in.var, static_cast<int>(blockIdx.x) >> 1);
+    if (vt.seq < 0) return;  // an empty slot (the whole cluster's)
+    p_var = p_in;
+    localize(p_var, vt);
+  }
+  const BwdParams& p = VAR ? p_var : p_in;
   constexpr int SA = kSlotsA, SB = kSlotsB;
   constexpr int kHps = kSlot / kHalf;    // score-operand half-chunks per slot
   constexpr int kResBytes = NC * kHalf;  // one resident operand: 64 rows x D columns
@@ -154,17 +166,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank();  // 0 issues the pair's MMAs
-  const Geo g = make_geo(p, static_cast<int>(rank));
+  const Geo g = make_geo<VAR>(p, vt, static_cast<int>(rank));
   uint32_t* status = p.status;
   auto lead = [&](int i) { return rank == 0 ? bar(i) : mapa(bar(i), 0); };
 
   // resident A1 = Q, A2 = dO (64-row halves); score operands B1 = K, B2 = V
   // (64-row halves); dQ operand B3 = K (128 rows, MN-major)
-  const CUtensorMap* mA1 = &map_qh;
-  const CUtensorMap* mA2 = &map_doh;
-  const CUtensorMap* mB1 = &map_kh;
-  const CUtensorMap* mB2 = &map_vh;
-  const CUtensorMap* mB3 = &map_k;
+  const CUtensorMap* mA1 = VAR ? var_map(p.var, vt, 0) : &map_qh;
+  const CUtensorMap* mA2 = VAR ? var_map(p.var, vt, 3) : &map_doh;
+  const CUtensorMap* mB1 = VAR ? var_map(p.var, vt, 1) : &map_kh;
+  const CUtensorMap* mB2 = VAR ? var_map(p.var, vt, 2) : &map_vh;
+  const CUtensorMap* mB3 = VAR ? var_map(p.var, vt, 4) : &map_k;
 
   if (tid == 0) {
     for (int i = 0; i < SA; ++i) {
@@ -209,6 +221,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int S = is_a ? SA : SB;
     const int full0 = is_a ? bl.full_a : bl.full_b, empty0 = is_a ? bl.empty_a : bl.empty_b;
     const uint32_t ring = is_a ? ring_a : ring_b;
+    if constexpr (VAR) {
+      var_map_acquire(mB3);
+      var_map_acquire(is_a ? mB1 : mB2);
+      var_map_acquire(mA1);
+      var_map_acquire(mA2);
+    }
     tma_prefetch_desc(mB3);
     tma_prefetch_desc(is_a ? mB1 : mB2);
     if (is_a) {
@@ -376,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t p_ready0 = bar(rank == 0 ? bl.p_ready : bl.p_local);  // local: the first CTA's or the relay's
     float lse2_row, delta_row;
     {
-      const int64_t idx = (static_cast<int64_t>(g.b) * p.Hq + g.h) * p.Nq + min(srow, p.Nq - 1);
+      const int64_t idx = (static_cast<int64_t>(g.b) * p.Hq + g.h) * stat_rows<VAR>(p) + min(srow, p.Nq - 1);
       lse2_row = p.lse2[idx];
       delta_row = p.delta[idx];
     }
@@ -539,11 +557,13 @@ cudaError_t launch_impl(const BwdParams& p, const BwdMaps& m, cudaStream_t st) {
   constexpr int smem = smem_bytes(NC);
   static_assert(smem <= 232448, "shared memory per CTA");
   static_assert(grad_cols(NC) <= 256, "dQ below the score buffers");
-  auto kern = p.dropout ? bwd_dq_kernel<NC, BF16, true> : bwd_dq_kernel<NC, BF16, false>;
+  auto kern = p.var.tiles ? bwd_dq_kernel<NC, BF16, false, true>
+              : p.dropout ? bwd_dq_kernel<NC, BF16, true, false>
+                          : bwd_dq_kernel<NC, BF16, false, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * p.q_tiles, p.Hq, p.B);
+  cfg.gridDim = dim3(2 * (p.var.tiles ? p.var.slots : p.q_tiles), p.Hq, p.B);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

@@ -72,6 +72,7 @@
 #include "internal.h"
 #include "philox.cuh"
 #include "ptx.cuh"
+#include "varlen.cuh"
 
 namespace ffpa {
 namespace {
@@ -170,8 +171,8 @@ struct Geo {
   int ncols, rot;      // column tiles and the sweep's start
 };
 
-template <int MODE, int NC>
-__device__ __forceinline__ Geo make_geo(const BwdParams& p, int pr, bool is_b) {
+template <int MODE, int NC, bool VAR>
+__device__ __forceinline__ Geo make_geo(const BwdParams& p, const VarTile& vt, int pr, bool is_b) {
   using G = Shape<NC>;
   Geo g;
   g.b = blockIdx.z;
@@ -179,7 +180,9 @@ __device__ __forceinline__ Geo make_geo(const BwdParams& p, int pr, bool is_b) {
   int gsel;
   if (MODE == kDKV) {
     gsel = G::kSplitKV == 2 ? (cl & 1) : 0;  // above D = 512 two clusters per key tile
-    g.st = cl / G::kSplitKV;
+    // packed: the slots are in the order of the query tiles' work; key tile
+    // kv_tiles - 1 - t of a causal sequence has the work of query tile t
+    g.st = VAR ? p.kv_tiles - 1 - vt.tile : cl / G::kSplitKV;
     g.kvh = blockIdx.y;
     g.hs = g.kvh;
     g.s_limit = p.Nkv;
@@ -188,7 +191,7 @@ __device__ __forceinline__ Geo make_geo(const BwdParams& p, int pr, bool is_b) {
     g.ncols = p.group * g.nq_h;
   } else {
     gsel = is_b ? 1 : 0;  // each pair accumulates one range of dQ's columns
-    g.st = p.q_tiles - 1 - cl;  // heavy causal tiles first
+    g.st = VAR ? vt.tile : p.q_tiles - 1 - cl;  // heavy causal tiles first
     g.hs = blockIdx.y;
     g.kvh = g.hs / p.group;
     g.s_limit = p.Nq;
@@ -221,12 +224,22 @@ __device__ __forceinline__ void column(const Geo& g, const BwdParams& p, int c, 
   }
 }
 
-template <int MODE, int NC, bool BF16, bool DROP>
+template <int MODE, int NC, bool BF16, bool DROP, bool VAR>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_xch_kernel(const __grid_constant__ CUtensorMap map_qh, const __grid_constant__ CUtensorMap map_kh,
                    const __grid_constant__ CUtensorMap map_vh, const __grid_constant__ CUtensorMap map_doh,
-                   const __grid_constant__ BwdParams p) {
+                   const __grid_constant__ BwdParams p_in) {
   using G = Shape<NC>;
+  // packed sequences: this cluster's sequence and tile, and the call's parameters for that sequence
+  VarTile vt = {};
+  BwdParams p_var;
+  if constexpr (VAR) {
+    vt = var_tile(p_in.var, (static_cast<int>(blockIdx.x) >> 2) / (MODE == kDKV ? G::kSplitKV : 1));
+    if (vt.seq < 0) return;  // an empty slot (the whole cluster's)
+    p_var = p_in;
+    localize(p_var, vt);
+  }
+  const BwdParams& p = VAR ? p_var : p_in;
   constexpr int kSlots = G::kSlots, kNrecv = G::kNrecv;
   constexpr bool DQ = MODE == kDQ;
   constexpr Bars bl = bar_layout();
@@ -244,16 +257,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t pr = rank & 1, lead_rank = rank & 2, other = rank ^ 2;  // other: same rows, other pair
   const uint16_t pair_mask = static_cast<uint16_t>(3u << lead_rank);
   const uint16_t other_mask = static_cast<uint16_t>(3u << (lead_rank ^ 2));
-  const Geo g = make_geo<MODE, NC>(p, static_cast<int>(pr), is_b);
+  const Geo g = make_geo<MODE, NC, VAR>(p, vt, static_cast<int>(pr), is_b);
   uint32_t* status = p.status;
   auto lead = [&](int i) { return pr == 0 ? bar(i) : mapa(bar(i), lead_rank); };
   // pair B's gradient operand in dQ mode is its own staging tile
   const bool own_operand = DQ && is_b;
 
   // stationary tile, score-product column operand (K-major), gradient column operand (MN-major)
-  const CUtensorMap* mRes = DQ ? (is_b ? &map_doh : &map_qh) : (is_b ? &map_vh : &map_kh);
-  const CUtensorMap* mX = DQ ? (is_b ? &map_vh : &map_kh) : (is_b ? &map_doh : &map_qh);
-  const CUtensorMap* mG = DQ ? &map_kh : (is_b ? &map_doh : &map_qh);
+  const CUtensorMap* m_qh = VAR ? var_map(p.var, vt, 0) : &map_qh;
+  const CUtensorMap* m_kh = VAR ? var_map(p.var, vt, 1) : &map_kh;
+  const CUtensorMap* m_vh = VAR ? var_map(p.var, vt, 2) : &map_vh;
+  const CUtensorMap* m_doh = VAR ? var_map(p.var, vt, 3) : &map_doh;
+  const CUtensorMap* mRes = DQ ? (is_b ? m_doh : m_qh) : (is_b ? m_vh : m_kh);
+  const CUtensorMap* mX = DQ ? (is_b ? m_vh : m_kh) : (is_b ? m_doh : m_qh);
+  const CUtensorMap* mG = DQ ? m_kh : (is_b ? m_doh : m_qh);
 
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
@@ -308,12 +325,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int full0 = is_x ? bl.full_x : bl.full_g, empty0 = is_x ? bl.empty_x : bl.empty_g;
     const uint32_t ring = is_x ? ring_x : ring_g;
     if (is_x) {
+      if constexpr (VAR) {
+        var_map_acquire(mRes);
+        var_map_acquire(mX);
+      }
       tma_prefetch_desc(mRes);
       tma_prefetch_desc(mX);
       if (pr == 0) mbar_expect_tx(bar(bl.res_full), 2 * G::kRes);
       for (int c = 4; c < NC; ++c)
         tma_load_4d_pair(res_sm + (c - 4) * kHalf, mRes, lead(bl.res_full), c * kChunk, g.s_row0, g.hs, g.b);
     } else {
+      if constexpr (VAR) var_map_acquire(mG);
       tma_prefetch_desc(mG);
     }
     bool ok = true;
@@ -545,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // dQ mode: the row statistics of this thread's query row
     float row_stat = 0.f;
     if (DQ) {
-      const int64_t idx = (static_cast<int64_t>(g.b) * p.Hq + g.hs) * p.Nq + min(srow, p.Nq - 1);
+      const int64_t idx = (static_cast<int64_t>(g.b) * p.Hq + g.hs) * stat_rows<VAR>(p) + min(srow, p.Nq - 1);
       row_stat = is_b ? p.delta[idx] : p.lse2[idx];
     }
     // dK/dV mode: column statistics of a column tile; lane l holds those of
@@ -555,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto load_stats = [&](int c, float (&dst)[2]) {
       int ch, cr0;
       column<MODE>(g, p, c, &ch, &cr0);
-      const int64_t sbase = (static_cast<int64_t>(g.b) * p.Hq + ch) * p.Nq;
+      const int64_t sbase = (static_cast<int64_t>(g.b) * p.Hq + ch) * stat_rows<VAR>(p);
 #pragma unroll
       for (int k2 = 0; k2 < 2; ++k2) dst[k2] = stat_vec[sbase + min(cr0 + 64 * u + 32 * k2 + lane, p.Nq - 1)];
     };
@@ -801,12 +823,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int MODE, int NC, bool BF16>
 cudaError_t launch_impl(const BwdParams& p, const BwdMaps& m, cudaStream_t st) {
   constexpr int smem = Shape<NC>::kSmemBytes;
-  auto kern = p.dropout ? bwd_xch_kernel<MODE, NC, BF16, true> : bwd_xch_kernel<MODE, NC, BF16, false>;
+  auto kern = p.var.tiles ? bwd_xch_kernel<MODE, NC, BF16, false, true>
+              : p.dropout ? bwd_xch_kernel<MODE, NC, BF16, true, false>
+                          : bwd_xch_kernel<MODE, NC, BF16, false, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   // dK/dV: one or two clusters per key tile (one per range of gradient columns); dQ: one per query tile
-  cfg.gridDim = MODE == kDKV ? dim3(4 * Shape<NC>::kSplitKV * p.kv_tiles, p.Hkv, p.B) : dim3(4 * p.q_tiles, p.Hq, p.B);
+  const int slots = p.var.tiles ? p.var.slots : (MODE == kDKV ? p.kv_tiles : p.q_tiles);
+  cfg.gridDim = MODE == kDKV ? dim3(4 * Shape<NC>::kSplitKV * slots, p.Hkv, p.B) : dim3(4 * slots, p.Hq, p.B);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

@@ -52,6 +52,7 @@
 #include "internal.h"
 #include "philox.cuh"
 #include "ptx.cuh"
+#include "varlen.cuh"
 
 namespace ffpa {
 namespace {
@@ -163,11 +164,22 @@ __device__ __forceinline__ bool pair_bar_and(uint32_t id, bool v) {
   return r != 0;
 }
 
-template <int NC, bool BF16, bool KSPLIT, bool DROP>
+template <int NC, bool BF16, bool KSPLIT, bool DROP, bool VAR>
 __global__ void __launch_bounds__(kThreads, 1)
     fwd_fulld_kernel(const __grid_constant__ CUtensorMap map_qh, const __grid_constant__ CUtensorMap map_kh,
-                     const __grid_constant__ CUtensorMap map_v, const __grid_constant__ FwdParams p) {
+                     const __grid_constant__ CUtensorMap map_v, const __grid_constant__ FwdParams p_in) {
   using G = Shape<NC>;
+  // packed sequences: this pair's sequence and tile, and the call's parameters for that sequence
+  VarTile vt = {};
+  FwdParams p_var;
+  if constexpr (VAR) {
+    vt = var_tile(p_in.var, static_cast<int>(blockIdx.x >> 1) / G::kNsplit);
+    if (vt.seq < 0) return;  // an empty slot (the whole cluster's)
+    p_var = p_in;
+    localize(p_var, vt);
+  }
+  const FwdParams& p = VAR ? p_var : p_in;
+
   constexpr int kQBytes = G::kQBytes, kOCols = G::kOCols, kQtc = G::kQtc, kNpb = G::kNpb;
   constexpr uint32_t kS0 = G::kS0, kS1 = G::kS1, kQt = G::kQt;
   constexpr int kPOff = G::kPOff, kRingKOff = G::kRingKOff, kRingVOff = G::kRingVOff, kMiscOff = G::kMiscOff;
@@ -193,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kvs = KSPLIT ? pair0 % p.kv_splits : 0;  // key split of this pair (KSPLIT: short query sets)
   const int pair = KSPLIT ? pair0 / p.kv_splits : pair0;
   const int split = pair % G::kNsplit;
-  const int qt = p.q_tiles - 1 - pair / G::kNsplit;  // heavy causal tiles first
+  const int qt = VAR ? vt.tile : p.q_tiles - 1 - pair / G::kNsplit;  // heavy causal tiles first
   const int q0 = qt * kTileRows;
   // this pair's O columns [o0, o0 + ow): halves of nv0 and nv1 64-column chunks per CTA
   const int o0 = split * G::kOw, ow = min(G::kOw, G::kD - o0);
@@ -209,6 +221,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             : (kv_end + kTileRows - 1) / kTileRows;
   uint32_t* status = p.status;
   auto lead = [&](int i) { return rank == 0 ? bar(i) : mapa(bar(i), 0); };
+  const CUtensorMap* m_qh = VAR ? var_map(p.var, vt, 0) : &map_qh;
+  const CUtensorMap* m_kh = VAR ? var_map(p.var, vt, 1) : &map_kh;
+  const CUtensorMap* m_v = VAR ? var_map(p.var, vt, 2) : &map_v;
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -253,14 +268,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ring = is_k ? ring_k : ring_v;
     const uint32_t S = is_k ? kKSlots : G::kVSlots;
     if (is_k) {
-      tma_prefetch_desc(&map_qh);
-      tma_prefetch_desc(&map_kh);
+      if constexpr (VAR) {
+        var_map_acquire(m_qh);
+        var_map_acquire(m_kh);
+      }
+      tma_prefetch_desc(m_qh);
+      tma_prefetch_desc(m_kh);
       if (rank == 0) mbar_expect_tx(bar(bl.q_full), 2 * kQBytes);
       for (int c = kQtc; c < NC; ++c)
-        tma_load_4d_pair(q_sm + (c - kQtc) * kHalfBytes, &map_qh, lead(bl.q_full), c * kChunk,
+        tma_load_4d_pair(q_sm + (c - kQtc) * kHalfBytes, m_qh, lead(bl.q_full), c * kChunk,
                          q0 + 64 * static_cast<int>(rank), h, b);
     } else {
-      tma_prefetch_desc(&map_v);
+      if constexpr (VAR) var_map_acquire(m_v);
+      tma_prefetch_desc(m_v);
     }
     bool ok = true;
     uint32_t it = 0;
@@ -278,11 +298,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t dst = ring + s * kSlotBytes, fb = lead(full0 + s);
       if (is_k) {
         for (int i = 0; i < nk; ++i)
-          tma_load_4d_pair(dst + i * kHalfBytes, &map_kh, fb, (4 * m + i) * kChunk,
+          tma_load_4d_pair(dst + i * kHalfBytes, m_kh, fb, (4 * m + i) * kChunk,
                            (t0 + j) * kTileRows + 64 * static_cast<int>(rank), kvh, b);
       } else {
         for (int i = 0; i < nv; ++i)
-          tma_load_4d_pair(dst + i * kChunkBytes, &map_v, fb, o0 + (4 * m + nv * static_cast<int>(rank) + i) * kChunk,
+          tma_load_4d_pair(dst + i * kChunkBytes, m_v, fb, o0 + (4 * m + nv * static_cast<int>(rank) + i) * kChunk,
                            (t0 + j) * kTileRows, kvh, b);
       }
     }
@@ -692,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (kh == 0 && split == 0 && p.lse && row < p.Nq) {
           constexpr float kLn2 = 0.6931471805599453f;
-          p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.Nq + row] =
+          p.lse[(static_cast<int64_t>(b) * p.Hq + h) * stat_rows<VAR>(p) + row] =
               l_sum > 0.f ? (m_used + __log2f(l_sum)) * kLn2 : -INFINITY;
         }
       }
@@ -716,13 +736,16 @@ cudaError_t launch_impl(const FwdParams& p_in, const FwdMaps& m, cudaStream_t st
   p.stages = kKSlots + Shape<NC>::kVSlots;
   p.slot_chunks = 2;
   // key splits and dropout are not combined (the host takes no key split with dropout)
-  auto kern = p.part_o ? fwd_fulld_kernel<NC, BF16, true, false>
-                       : (p.dropout ? fwd_fulld_kernel<NC, BF16, false, true> : fwd_fulld_kernel<NC, BF16, false, false>);
+  auto kern = p.var.tiles ? fwd_fulld_kernel<NC, BF16, false, false, true>
+              : p.part_o  ? fwd_fulld_kernel<NC, BF16, true, false, false>
+              : p.dropout ? fwd_fulld_kernel<NC, BF16, false, true, false>
+                          : fwd_fulld_kernel<NC, BF16, false, false, false>;
   constexpr int kNsplit = Shape<NC>::kNsplit;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * p.q_tiles * kNsplit * (p.part_o ? p.kv_splits : 1), p.Hq, p.B);  // (pair rank, key split, O split, query tile)
+  const int slots = p.var.tiles ? p.var.slots : p.q_tiles;
+  cfg.gridDim = dim3(2 * slots * kNsplit * (p.part_o ? p.kv_splits : 1), p.Hq, p.B);  // (pair rank, key split, O split, query tile)
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = st;

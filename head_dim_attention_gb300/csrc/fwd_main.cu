@@ -22,6 +22,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "varlen.cuh"
 
 namespace ffpa {
 namespace {
@@ -85,10 +86,20 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   }
 }
 
-template <bool BF16>
+template <bool BF16, bool VAR>
 __global__ void __launch_bounds__(kThreads, 1)
     fwd_main_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                    const __grid_constant__ CUtensorMap map_v, const __grid_constant__ FwdParams p) {
+                    const __grid_constant__ CUtensorMap map_v, const __grid_constant__ FwdParams p_in) {
+  // packed sequences: this block's sequence and tile, and the call's parameters for that sequence
+  VarTile vt = {};
+  FwdParams p_var;
+  if constexpr (VAR) {
+    vt = var_tile(p_in.var, static_cast<int>(blockIdx.x));
+    if (vt.seq < 0) return;  // an empty slot
+    p_var = p_in;
+    localize(p_var, vt);
+  }
+  const FwdParams& p = VAR ? p_var : p_in;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int stages = p.stages;
@@ -106,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t q_sm = s_base + plan.q_off, ring_sm = s_base + plan.ring_off;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int qt = p.q_tiles - 1 - static_cast<int>(blockIdx.x);  // heavy causal tiles first
+  const int qt = VAR ? vt.tile : p.q_tiles - 1 - static_cast<int>(blockIdx.x);  // heavy causal tiles first
   const int h = blockIdx.y, b = blockIdx.z;
   const int kvh = h / p.group;
   const int q0 = qt * kTileRows;
@@ -114,6 +125,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kv_end = p.causal ? min(p.Nkv, q0 + kTileRows) : p.Nkv;
   const int ntiles = (kv_end + kTileRows - 1) / kTileRows;
   uint32_t* status = p.status;
+  const CUtensorMap* m_q = VAR ? var_map(p.var, vt, 0) : &map_q;
+  const CUtensorMap* m_k = VAR ? var_map(p.var, vt, 1) : &map_k;
+  const CUtensorMap* m_v = VAR ? var_map(p.var, vt, 2) : &map_v;
 
   if (tid == 0) {
     for (int i = 0; i < stages; ++i) {
@@ -153,12 +167,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nprod = min(kProducers, stages);
     const int pi = (warp == 0) ? 0 : warp - 1;
     if (lane == 0 && pi < nprod) {
-      tma_prefetch_desc(&map_q);
-      tma_prefetch_desc(&map_k);
-      tma_prefetch_desc(&map_v);
+      if constexpr (VAR) {
+        var_map_acquire(m_q);
+        var_map_acquire(m_k);
+        var_map_acquire(m_v);
+      }
+      tma_prefetch_desc(m_q);
+      tma_prefetch_desc(m_k);
+      tma_prefetch_desc(m_v);
       if (pi == 0) {
         mbar_expect_tx(bar(bl.q_full), n * kChunkBytes);
-        for (int c = 0; c < n; ++c) tma_load_4d(q_sm + c * kChunkBytes, &map_q, bar(bl.q_full), c * kChunk, q0, h, b);
+        for (int c = 0; c < n; ++c) tma_load_4d(q_sm + c * kChunkBytes, m_q, bar(bl.q_full), c * kChunk, q0, h, b);
       }
       bool ok = true;
       uint32_t it = 0;
@@ -182,9 +201,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // K of tile j, then V of tile j - 1: the order the MMA thread uses them
       for (int j = 0; j <= ntiles && ok; ++j) {
         if (j < ntiles)
-          for (int c = 0; c < n; c += G) load(&map_k, c, min(G, n - c), j * kTileRows);
+          for (int c = 0; c < n; c += G) load(m_k, c, min(G, n - c), j * kTileRows);
         if (j >= 1)
-          for (int c = 0; c < n; c += G) load(&map_v, c, min(G, n - c), (j - 1) * kTileRows);
+          for (int c = 0; c < n; c += G) load(m_v, c, min(G, n - c), (j - 1) * kTileRows);
       }
       // Drain: wait for the last release of each ring slot whose last load was
       // ours. The MMA warp's commit arrives on empty[s] only when the MMAs
@@ -486,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (p.lse && row < p.Nq) {
         constexpr float kLn2 = 0.6931471805599453f;
-        p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.Nq + row] =
+        p.lse[(static_cast<int64_t>(b) * p.Hq + h) * stat_rows<VAR>(p) + row] =
             l_sum > 0.f ? (m_used + __log2f(l_sum)) * kLn2 : -INFINITY;
       }
     }
@@ -515,11 +534,11 @@ cudaError_t launch_impl(const FwdParams& p_in, const FwdMaps& m, cudaStream_t st
   p.slot_chunks = G;
   const SmemPlan plan = smem_plan(p.n_chunks, stages, G);
   const int smem = plan.total + 1024;  // + alignment slack
-  auto kern = fwd_main_kernel<BF16>;
+  auto kern = p.var.tiles ? fwd_main_kernel<BF16, true> : fwd_main_kernel<BF16, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.q_tiles, p.Hq, p.B);
+  cfg.gridDim = dim3(p.var.tiles ? p.var.slots : p.q_tiles, p.Hq, p.B);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

@@ -44,6 +44,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "varlen.cuh"
 
 namespace ffpa {
 namespace {
@@ -149,11 +150,22 @@ __device__ __forceinline__ bool pair_bar_and(uint32_t id, bool v) {
   return r != 0;
 }
 
-template <int NC, bool BF16>
+template <int NC, bool BF16, bool VAR>
 __global__ void __launch_bounds__(kThreads, 1)
     fwd_xch_kernel(const __grid_constant__ CUtensorMap map_qh, const __grid_constant__ CUtensorMap map_kh,
-                   const __grid_constant__ CUtensorMap map_v, const __grid_constant__ FwdParams p) {
+                   const __grid_constant__ CUtensorMap map_v, const __grid_constant__ FwdParams p_in) {
   using G = Shape<NC>;
+  // packed sequences: this cluster's sequence and tile, and the call's parameters for that sequence
+  VarTile vt = {};
+  FwdParams p_var;
+  if constexpr (VAR) {
+    vt = var_tile(p_in.var, static_cast<int>(blockIdx.x >> 2));
+    if (vt.seq < 0) return;  // an empty slot (the whole cluster's)
+    p_var = p_in;
+    localize(p_var, vt);
+  }
+  const FwdParams& p = VAR ? p_var : p_in;
+
   constexpr int kQtc = G::kQtc, kSlots = G::kSlots, kSlotsB = G::kSlotsB, kNblk = G::kNblk;
   constexpr Bars bl = bar_layout();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -177,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t ring = base + (is_b ? G::kRingOffB : G::kRingOff);
   const uint16_t pair_mask = static_cast<uint16_t>(3u << lead_rank);
   const uint16_t other_mask = static_cast<uint16_t>(3u << (lead_rank ^ 2));
-  const int qt = p.q_tiles - 1 - static_cast<int>(blockIdx.x >> 2);  // heavy causal tiles first
+  const int qt = VAR ? vt.tile : p.q_tiles - 1 - static_cast<int>(blockIdx.x >> 2);  // heavy causal tiles first
   const int q0 = qt * kTileRows;
   const int h = blockIdx.y, b = blockIdx.z;
   const int kvh = h / p.group;
@@ -185,6 +197,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int ntiles = (kv_end + kTileRows - 1) / kTileRows;
   uint32_t* status = p.status;
   auto lead = [&](int i) { return pr == 0 ? bar(i) : mapa(bar(i), lead_rank); };
+  const CUtensorMap* m_qh = VAR ? var_map(p.var, vt, 0) : &map_qh;
+  const CUtensorMap* m_kh = VAR ? var_map(p.var, vt, 1) : &map_kh;
+  const CUtensorMap* m_v = VAR ? var_map(p.var, vt, 2) : &map_v;
 
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
@@ -225,11 +240,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     // This CTA's slot s is free once the pair's MMAs reading it completed (the
     // first CTA's commit arrives here); the bytes of both CTAs are counted on
     // the first CTA's full[s].
-    tma_prefetch_desc(&map_qh);
-    tma_prefetch_desc(&map_kh);
+    if constexpr (VAR) {
+      var_map_acquire(m_qh);
+      var_map_acquire(m_kh);
+    }
+    tma_prefetch_desc(m_qh);
+    tma_prefetch_desc(m_kh);
     if (pr == 0) mbar_expect_tx(bar(bl.q_full), 2 * G::kQBytes);
     for (int c = kQtc; c < NC; ++c)
-      tma_load_4d_pair(q_sm + (c - kQtc) * kHalfBytes, &map_qh, lead(bl.q_full), c * kChunk,
+      tma_load_4d_pair(q_sm + (c - kQtc) * kHalfBytes, m_qh, lead(bl.q_full), c * kChunk,
                        q0 + 64 * static_cast<int>(pr), h, b);
     bool ok = true;
     uint32_t it = 0;
@@ -243,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (pr == 0) mbar_expect_tx(bar(bl.full_r + s), 2 * nk * kHalfBytes);
       const uint32_t dst = ring + s * kSlotBytes, fb = lead(bl.full_r + s);
       for (int i = 0; i < nk; ++i)
-        tma_load_4d_pair(dst + i * kHalfBytes, &map_kh, fb, (4 * m + i) * kChunk,
+        tma_load_4d_pair(dst + i * kHalfBytes, m_kh, fb, (4 * m + i) * kChunk,
                          j * kTileRows + 64 * static_cast<int>(pr), kvh, b);
     }
     for (uint32_t s = 0; s < static_cast<uint32_t>(kSlots) && s < it && ok; ++s) {
@@ -254,7 +273,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ pair B: the V ring
     // one slot per O block and key tile: this CTA's half of the block's
     // columns (one or two 64-column chunks) over the tile's 128 keys
-    tma_prefetch_desc(&map_v);
+    if constexpr (VAR) var_map_acquire(m_v);
+    tma_prefetch_desc(m_v);
     bool ok = true;
     uint32_t it = 0;
     for (int n = 0; n < kNblk * ntiles && ok; ++n) {
@@ -268,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (pr == 0) mbar_expect_tx(bar(bl.full_r + s), 2 * nv * kChunkBytes);
       const uint32_t dst = ring + s * kSlotBytes, fb = lead(bl.full_r + s);
       for (int i = 0; i < nv; ++i)
-        tma_load_4d_pair(dst + i * kChunkBytes, &map_v, fb, 256 * nb + (nv * static_cast<int>(pr) + i) * kChunk,
+        tma_load_4d_pair(dst + i * kChunkBytes, m_v, fb, 256 * nb + (nv * static_cast<int>(pr) + i) * kChunk,
                          j * kTileRows, kvh, b);
     }
     for (uint32_t s = 0; s < static_cast<uint32_t>(kSlotsB) && s < it && ok; ++s) {
@@ -576,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (kh == 0 && p.lse && row < p.Nq) {
       constexpr float kLn2 = 0.6931471805599453f;
-      p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.Nq + row] =
+      p.lse[(static_cast<int64_t>(b) * p.Hq + h) * stat_rows<VAR>(p) + row] =
           l_sum > 0.f ? (m_used + __log2f(l_sum)) * kLn2 : -INFINITY;
     }
   } else if (is_b && warp >= 4) {
@@ -676,11 +696,11 @@ template <int NC, bool BF16>
 cudaError_t launch_impl(const FwdParams& p_in, const FwdMaps& m, cudaStream_t st) {
   constexpr int kSmemBytes = Shape<NC>::kSmemBytes;
   FwdParams p = p_in;
-  auto kern = fwd_xch_kernel<NC, BF16>;
+  auto kern = p.var.tiles ? fwd_xch_kernel<NC, BF16, true> : fwd_xch_kernel<NC, BF16, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(4 * p.q_tiles, p.Hq, p.B);  // (CTA of the cluster, query tile)
+  cfg.gridDim = dim3(4 * (p.var.tiles ? p.var.slots : p.q_tiles), p.Hq, p.B);  // (CTA of the cluster, query tile)
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = st;

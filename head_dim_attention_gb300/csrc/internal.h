@@ -12,11 +12,33 @@ enum : uint32_t {
   FFPA_DEV_OK = 0,
   FFPA_DEV_TIMEOUT = 1,
   FFPA_DEV_LAYOUT = 2,  // dynamic shared memory not on the boundary a kernel's layout needs
+  FFPA_DEV_LENGTHS = 3, // lengths, starts, page or slot numbers in device memory out of their range
 };
 
 constexpr int kTileRows = 128;  // query/key rows per tile (the MMA M)
 constexpr int kChunk = 64;      // D columns per chunk (one 128-byte swizzled row)
 constexpr int kChunkBytes = kTileRows * kChunk * 2;  // 16 KB
+
+// Packed sequences (varlen.cuh).
+constexpr int kVarMaps = 5;  // TMA maps per sequence, at most
+struct VarParams {
+  const int4* tiles;        // [slots] (sequence or -1, tile, first row, length); nullptr: not a packed call
+  const CUtensorMap* maps;  // [sequences][kVarMaps]
+  int slots;                // blocks (or clusters) along x per head
+  int total;                // rows of q, k and v: the head stride of lse, delta and lse2
+};
+struct VarPlan {
+  CUtensorMap maps[kVarMaps];    // of the whole packed tensors
+  const void* base[kVarMaps];    // their data pointers
+  int64_t row_stride[kVarMaps];  // elements
+  int n_maps;
+  const int32_t* cu;             // [n_seqs + 1] first rows, ascending
+  int n_seqs, total, slots, causal;
+  int bin_shift;                 // work classes of 2^bin_shift key tiles
+  int4* tiles;
+  CUtensorMap* out_maps;
+  uint32_t* status;
+};
 
 // Forward, fused tcgen05 path.
 struct FwdParams {
@@ -43,6 +65,7 @@ struct FwdParams {
   int kv_splits, kv_split_tiles;
   float* part_o;      // [B, Hq, Nq, kv_splits, D] fp32
   float* part_ml;     // [B, Hq, Nq, kv_splits, 2] fp32 (max, sum), log2 domain
+  VarParams var;      // packed sequences
   // dropout (philox.cuh): on when `dropout` is set; keep threshold, seed words,
   // stream offset and the multiplier 1 / (1 - p) of kept probabilities
   int dropout;
@@ -114,6 +137,7 @@ struct BwdParams {
   int slot_chunks;    // 16 KB tiles per ring slot (1 or 2), loaded under one barrier phase
   int q_tiles, kv_tiles;
   uint32_t* status;
+  VarParams var;      // packed sequences
   // dropout, as in FwdParams
   int dropout;
   uint32_t drop_t, drop_seed_lo, drop_seed_hi, drop_off;
@@ -126,6 +150,9 @@ struct BwdMaps {
 };
 
 bool dtype_is_bf16(int dtype);
+
+// Fills the tile slots and the per-sequence maps of a packed call (varlen.cu).
+cudaError_t launch_varlen_plan(const VarPlan& p, cudaStream_t s);
 
 cudaError_t launch_fwd_main(const FwdParams& p, const FwdMaps& m, bool bf16, cudaStream_t s);
 // Full-D CTA-pair forward (fwd_fulld.cu): D = 512, one pair holds all of O.

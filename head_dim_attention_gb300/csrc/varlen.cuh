@@ -1,0 +1,76 @@
+// Packed sequences: what the attention kernels share when the rows of q, k
+// and v are several sequences one after the other.
+//
+// A sequence is treated as a tensor of its own.  Every TMA map a kernel uses is
+// copied once per sequence with its base moved to the sequence's first row and
+// its row count set to the sequence's length (tensormap.replace, in the plan
+// kernel of varlen.cu), so rows of a neighbour are out of range: they arrive as
+// zeros, exactly as rows past the end of an unpacked tensor do, and neither a
+// value nor a NaN of one sequence can reach another.  With pointers moved and
+// Nq = Nkv = length (localize below) the kernels' index arithmetic is that of
+// an unpacked call with one batch.
+//
+// The host does not know the lengths.  It launches as many (sequence, tile)
+// slots as `n` sequences of `T` rows in all can have; the plan kernel fills the
+// slots, heaviest tile first, and a block whose slot is empty returns at once.
+#pragma once
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace ffpa {
+
+// One slot's sequence and 128-row tile.
+struct VarTile {
+  int seq;   // -1: empty slot
+  int tile;  // query tile; its work in a causal call is tile + 1 key tiles
+  int start, len;
+};
+
+__device__ __forceinline__ VarTile var_tile(const VarParams& v, int slot) {
+  const int4 t = __ldg(v.tiles + slot);
+  return VarTile{t.x, t.y, t.z, t.w};
+}
+
+__device__ __forceinline__ const CUtensorMap* var_map(const VarParams& v, const VarTile& t, int which) {
+  return v.maps + static_cast<int64_t>(t.seq) * kVarMaps + which;
+}
+
+// Before a thread's first use of a map that the plan kernel wrote.
+__device__ __forceinline__ void var_map_acquire(const CUtensorMap* m) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
+__device__ __forceinline__ void* var_rows(const void* base, int64_t rows, int64_t row_stride) {
+  return const_cast<uint16_t*>(static_cast<const uint16_t*>(base) + rows * row_stride);  // 16-bit elements
+}
+
+// The call's parameters as an unpacked call over one sequence would have them.
+__device__ __forceinline__ void localize(FwdParams& p, const VarTile& t) {
+  p.Nq = p.Nkv = t.len;
+  p.q_tiles = (t.len + kTileRows - 1) / kTileRows;
+  p.q = var_rows(p.q, t.start, p.q_sn);
+  p.out = var_rows(p.out, t.start, p.o_sn);
+  if (p.lse) p.lse += t.start;
+}
+
+__device__ __forceinline__ void localize(BwdParams& p, const VarTile& t) {
+  p.Nq = p.Nkv = t.len;
+  p.q_tiles = p.kv_tiles = (t.len + kTileRows - 1) / kTileRows;
+  p.q = var_rows(p.q, t.start, p.q_sn);
+  p.k = var_rows(p.k, t.start, p.k_sn);
+  p.v = var_rows(p.v, t.start, p.v_sn);
+  p.dout = var_rows(p.dout, t.start, p.do_sn);
+  p.dq = var_rows(p.dq, t.start, p.dq_sn);
+  p.dk = var_rows(p.dk, t.start, p.dk_sn);
+  p.dv = var_rows(p.dv, t.start, p.dv_sn);
+  p.delta += t.start;
+  p.lse2 += t.start;
+}
+
+// Distance between the heads of lse, delta and lse2.
+template <bool VAR, class P>
+__device__ __forceinline__ int stat_rows(const P& p) {
+  return VAR ? p.var.total : p.Nq;
+}
+
+}  // namespace ffpa

@@ -152,6 +152,47 @@ int ffpa_bwd_dropout(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_
                      const ffpa_tensor_t* dv, ffpa_stream_t stream);
 
 /*
+ * ffpa_fwd_varlen / ffpa_bwd_varlen: ffpa_fwd and ffpa_bwd over sequences of
+ * different lengths packed one after the other (self-attention: as many keys
+ * as queries).  The pages have no counterpart; prompts of a serving batch and
+ * documents of a training step come in this form.
+ *
+ *   q, out, dout, dq  [1, Hq, T, D]    f16 or bf16
+ *   k, v, dk, dv      [1, Hkv, T, D]   Hkv divides Hq
+ *   lse               f32 [1, Hq, T, 1], contiguous (nullable in the forward)
+ *   cu_seqlens        device int32 [n_seqs + 1]: sequence s is rows
+ *                     cu_seqlens[s] .. cu_seqlens[s + 1] - 1
+ *   n_seqs            1 .. 2^20
+ *   causal            0 or 1: row i of a sequence sees its rows j <= i
+ *
+ * Strides are free as in ffpa_fwd, so token-major storage [T, H, D] is the
+ * view with head stride D.  A sequence may be empty.  Rows outside every
+ * sequence (before cu_seqlens[0], behind the last one) are neither read into
+ * a result nor written, and no value of one sequence, NaN included, reaches
+ * another.  Within a sequence the contract of ffpa_fwd / ffpa_bwd holds: a
+ * masked key has weight 0, so its values must be finite (0 times NaN is NaN in
+ * a matrix product).
+ *
+ * cu_seqlens is read on the device, so a captured call follows new lengths at
+ * every replay.  The entries must ascend within 0 .. T.  A pair that does not
+ * describes no sequence: its rows are not written, and ffpa_check_status
+ * returns FFPA_ERR_INVALID_ARG.  Ranges that overlap are not detected; their
+ * shared rows then hold either result.
+ *
+ * Two launches (forward: the plan, the attention kernel) or five (backward,
+ * D >= 320: four): the plan gives every block its sequence and tile.  Its
+ * scratch, (640 n_seqs + 16 slots) bytes for at most (T + 127 n_seqs) / 128
+ * slots, is stream-ordered on `stream` from the library's memory pool.
+ */
+int ffpa_fwd_varlen(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_tensor_t* v,
+                    const int32_t* cu_seqlens, int n_seqs, int causal, float scale, const ffpa_tensor_t* out,
+                    const ffpa_tensor_t* lse, ffpa_stream_t stream);
+int ffpa_bwd_varlen(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_tensor_t* v,
+                    const int32_t* cu_seqlens, int n_seqs, int causal, float scale, const ffpa_tensor_t* out,
+                    const ffpa_tensor_t* lse, const ffpa_tensor_t* dout, const ffpa_tensor_t* dq,
+                    const ffpa_tensor_t* dk, const ffpa_tensor_t* dv, ffpa_stream_t stream);
+
+/*
  * ffpa_fwd_decode_noalloc: the decode forward (Nq <= 16) without allocating.
  * The pages have no counterpart; it exists for callers that cannot allocate
  * device memory during the call: code running under another framework's
@@ -186,7 +227,9 @@ const char* ffpa_status_string(int status);
 /*
  * Synchronise `stream`, then read and clear the current device's status word.
  * Returns FFPA_ERR_TIMEOUT if a kernel's bounded wait expired since the last
- * check, FFPA_ERR_CUDA if the synchronisation failed, FFPA_OK otherwise.
+ * check, FFPA_ERR_INVALID_ARG if a kernel met lengths, starts, pages or slots
+ * in device memory that are out of range, FFPA_ERR_CUDA if the synchronisation
+ * failed, FFPA_OK otherwise.  The first error since the last check is kept.
  */
 int ffpa_check_status(ffpa_stream_t stream);
 
