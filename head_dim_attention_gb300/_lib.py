@@ -17,7 +17,8 @@ FFPA_F16, FFPA_BF16, FFPA_F32 = 0, 1, 2
 STATUS = {0: "FFPA_OK", 1: "FFPA_ERR_INVALID_ARG", 2: "FFPA_ERR_UNSUPPORTED", 3: "FFPA_ERR_ALIGNMENT",
           4: "FFPA_ERR_CUDA", 5: "FFPA_ERR_TIMEOUT", 6: "FFPA_ERR_SCRATCH_LIMIT"}
 EXPORTS = ("ffpa_fwd", "ffpa_bwd", "ffpa_fwd_dropout", "ffpa_bwd_dropout", "ffpa_fwd_decode_noalloc",
-           "ffpa_fwd_varlen", "ffpa_bwd_varlen", "ffpa_status_string", "ffpa_check_status",
+           "ffpa_fwd_varlen", "ffpa_bwd_varlen", "ffpa_fwd_tree", "ffpa_cache_plan", "ffpa_cache_append",
+           "ffpa_status_string", "ffpa_check_status",
            "ffpa_set_timing_events", "ffpa_selftest_wait_timeout", "ffpa_version")
 
 
@@ -62,6 +63,13 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.ffpa_fwd_varlen.restype = I
     lib.ffpa_bwd_varlen.argtypes = [P, P, P, V, I, I, F, P, P, P, P, P, P, V]
     lib.ffpa_bwd_varlen.restype = I
+    L = ctypes.c_int64
+    lib.ffpa_fwd_tree.argtypes = [P, P, P, V, I, V, V, V, I, F, P, P, V]
+    lib.ffpa_fwd_tree.restype = I
+    lib.ffpa_cache_plan.argtypes = [V, V, I, I, V, I, V, I, V, V, V, L, V, V, V]
+    lib.ffpa_cache_plan.restype = I
+    lib.ffpa_cache_append.argtypes = [P, P, P, P, V, V]
+    lib.ffpa_cache_append.restype = I
     lib.ffpa_status_string.argtypes = [ctypes.c_int]
     lib.ffpa_status_string.restype = ctypes.c_char_p
     lib.ffpa_check_status.argtypes = [ctypes.c_void_p]
@@ -222,6 +230,66 @@ def ffpa_bwd_varlen(q, k, v, cu_seqlens, causal, scale, out, lse, dout, dq, dk, 
     rc = lib.ffpa_bwd_varlen(*[_ref(x) for x in ds[:3]], cu, cu_seqlens.shape[0] - 1, int(causal), float(scale),
                              *[_ref(x) for x in ds[3:]], _stream(stream))
     _raise(rc)
+
+
+def _same(t, name, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def ffpa_fwd_tree(q, k_cache, v_cache, block_table, seq_lens, draft_lens, tree_mask, scale, out, lse,
+                  stream=None) -> None:
+    """Call ffpa_fwd_tree (drafted tokens over a paged cache); raises FfpaError on a non-zero status."""
+    lib = load()
+    table, lens = _ints(block_table, "block_table", 2), _ints(seq_lens, "seq_lens", 1)
+    drafts = None if draft_lens is None else _ints(draft_lens, "draft_lens", 1)
+    mask = None if tree_mask is None else _ints(tree_mask, "tree_mask", 3, "bool")
+    B, T = q.shape[0], q.shape[2]
+    _same(block_table, "block_table", (B, block_table.shape[1]))
+    _same(seq_lens, "seq_lens", (B,))
+    if draft_lens is not None:
+        _same(draft_lens, "draft_lens", (B,))
+    if tree_mask is not None:
+        _same(tree_mask, "tree_mask", (tree_mask.shape[0], T, T))
+    check_devices((q, k_cache, v_cache, block_table, seq_lens, draft_lens, tree_mask, out, lse), _current_device())
+    ds = [describe(x) for x in (q, k_cache, v_cache, out)] + [describe(lse, as_lse=True)]
+    rc = lib.ffpa_fwd_tree(*[_ref(x) for x in ds[:3]], table, block_table.shape[1], lens, drafts, mask,
+                           0 if tree_mask is None else tree_mask.shape[0], float(scale), _ref(ds[3]), _ref(ds[4]),
+                           _stream(stream))
+    _raise(rc)
+
+
+def ffpa_cache_plan(lens, new_lens, page_size, block_table, free_pages, free_head, cu_new, slots, lens_out,
+                    free_head_out, stream=None) -> None:
+    """Call ffpa_cache_plan (block tables and slots from request lengths); raises FfpaError on a non-zero status."""
+    lib = load()
+    n = lens.shape[0]
+    for t, name, shape in ((lens, "lens", (n,)), (new_lens, "new_lens", (n,)), (free_head, "free_head", (1,)),
+                           (cu_new, "cu_new", (n + 1,)), (lens_out, "lens_out", (n,)),
+                           (free_head_out, "free_head_out", (1,))):
+        _ints(t, name, 1)
+        _same(t, name, shape)
+    table = _ints(block_table, "block_table", 2)
+    _same(block_table, "block_table", (n, block_table.shape[1]))
+    pages, out_slots = _ints(free_pages, "free_pages", 1), _ints(slots, "slots", 1, "int64")
+    check_devices((lens, new_lens, block_table, free_pages, free_head, cu_new, slots, lens_out, free_head_out),
+                  _current_device())
+    at = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    rc = lib.ffpa_cache_plan(at(lens), at(new_lens), n, int(page_size), table, block_table.shape[1], pages,
+                             free_pages.shape[0], at(free_head), at(cu_new), out_slots, slots.shape[0], at(lens_out),
+                             at(free_head_out), _stream(stream))
+    _raise(rc)
+
+
+def ffpa_cache_append(k, v, k_cache, v_cache, slots, stream=None) -> None:
+    """Call ffpa_cache_append (rows of k and v into their slots); raises FfpaError on a non-zero status."""
+    lib = load()
+    where = _ints(slots, "slots", 1, "int64")
+    check_devices((k, v, k_cache, v_cache, slots), _current_device())
+    if slots.shape[0] != k.shape[2]:
+        raise ValueError(f"slots must have one entry per row of k, got {slots.shape[0]} for {k.shape[2]}")
+    ds = [describe(x) for x in (k, v, k_cache, v_cache)]
+    _raise(lib.ffpa_cache_append(*[_ref(x) for x in ds], where, _stream(stream)))
 
 
 def ffpa_check_status(stream=None) -> int:

@@ -642,6 +642,167 @@ int bwd_varlen_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_t
   return cuda_rc(e != cudaSuccess ? e : e2);
 }
 
+// ------------------------------------------------------------ paged cache
+constexpr int kMaxDrafts = 128;
+
+bool good_page(int64_t page) { return page == 16 || page == 32 || page == 64 || (page >= 128 && page % 128 == 0); }
+
+// [pages, Hkv, page, D] caches of one shape and type; the strides may differ.
+int check_caches(const ffpa_tensor_t* kc, const ffpa_tensor_t* vc, int dtype, int64_t D) {
+  if (!kc || !vc) return FFPA_ERR_INVALID_ARG;
+  const Shape4 want = {kc->shape[0], kc->shape[1], kc->shape[2], D};
+  if (want.B < 1 || want.H < 1 || want.N < 1) return FFPA_ERR_INVALID_ARG;
+  if (want.B > (1ll << 30) || want.H > 65535 || want.N > (1 << 20) || !good_page(want.N)) return FFPA_ERR_UNSUPPORTED;
+  int rc = check_bhnd(kc, dtype, want);
+  return rc ? rc : check_bhnd(vc, dtype, want);
+}
+
+int check_ints(const void* p, int bytes, bool required) {
+  if (!p) return required ? FFPA_ERR_INVALID_ARG : FFPA_OK;
+  return reinterpret_cast<uintptr_t>(p) % bytes ? FFPA_ERR_ALIGNMENT : FFPA_OK;
+}
+
+int fwd_tree_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* kc, const ffpa_tensor_t* vc, const int32_t* table,
+                  int max_pages, const int32_t* seq_lens, const int32_t* draft_lens, const uint8_t* mask, int mask_batch,
+                  float scale, const ffpa_tensor_t* out, const ffpa_tensor_t* lse, ffpa_stream_t stream) {
+  if (!q || !kc || !vc) return FFPA_ERR_INVALID_ARG;
+  if (!is_half_dtype(q->dtype)) return FFPA_ERR_UNSUPPORTED;
+  Common c;
+  c.dtype = q->dtype;
+  c.B = q->shape[0]; c.Hq = q->shape[1]; c.Nq = q->shape[2]; c.D = q->shape[3];
+  c.Hkv = kc->shape[1];
+  c.Nkv = 0;
+  if (c.B < 1 || c.Hq < 1 || c.Hkv < 1 || c.Nq < 1 || c.D < 1) return FFPA_ERR_INVALID_ARG;
+  if (c.B > 65535 || c.Hq > 65535 || c.Nq > kMaxDrafts) return FFPA_ERR_UNSUPPORTED;
+  if (c.Hq % c.Hkv != 0) return FFPA_ERR_INVALID_ARG;
+  if (c.D % 64 != 0 || c.D < 64 || c.D > 1024) return FFPA_ERR_UNSUPPORTED;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return FFPA_ERR_INVALID_ARG;
+  int rc;
+  if ((rc = check_bhnd(q, c.dtype, {c.B, c.Hq, c.Nq, c.D}))) return rc;
+  if ((rc = check_caches(kc, vc, c.dtype, c.D))) return rc;
+  if ((rc = check_bhnd(out, c.dtype, {c.B, c.Hq, c.Nq, c.D}))) return rc;
+  if (lse && (rc = check_lse(lse, c))) return rc;
+  if ((rc = check_ints(table, 4, true)) || (rc = check_ints(seq_lens, 4, true)) || (rc = check_ints(draft_lens, 4, false)))
+    return rc;
+  if (max_pages < 1 || (mask && mask_batch != 1 && mask_batch != c.B)) return FFPA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(max_pages) * kc->shape[2] > (1ll << 30)) return FFPA_ERR_UNSUPPORTED;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint32_t* status = device_status_word();
+  const int sms = device_sm_count();
+  if (!status || sms <= 0) return FFPA_ERR_CUDA;
+  TreeParams p = {};
+  p.q = q->data;
+  p.out = out->data;
+  p.lse = lse ? static_cast<float*>(lse->data) : nullptr;
+  p.q_sb = q->stride[0]; p.q_sh = q->stride[1]; p.q_sn = q->stride[2];
+  p.o_sb = out->stride[0]; p.o_sh = out->stride[1]; p.o_sn = out->stride[2];
+  p.table = table;
+  p.table_stride = max_pages;
+  p.seq_lens = seq_lens;
+  p.draft_lens = draft_lens;
+  p.mask = mask;
+  p.mask_sb = mask_batch == 1 ? 0 : c.Nq * c.Nq;
+  p.B = (int)c.B; p.Hq = (int)c.Hq; p.Hkv = (int)c.Hkv; p.T = (int)c.Nq; p.D = (int)c.D;
+  p.group = (int)(c.Hq / c.Hkv);
+  p.n_chunks = (int)(c.D / kChunk);
+  p.page = (int)kc->shape[2];
+  p.n_pages = (int)kc->shape[0];
+  p.max_pages = max_pages;
+  p.scale_log2 = scale * kLog2e;
+  const int64_t rows = static_cast<int64_t>(p.group) * p.T;
+  p.rows_n = tree_rows_n(static_cast<int>(std::min<int64_t>(rows, 1 << 20)), p.D);
+  // as many blocks as there can be key tiles to share out, one per SM at most
+  const int64_t units = c.B * c.Hkv * ((rows + p.rows_n - 1) / p.rows_n);
+  const int64_t tiles = (static_cast<int64_t>(max_pages) * p.page + kTileRows - 1) / kTileRows;
+  p.blocks = static_cast<int>(units >= sms || tiles >= sms ? sms : std::min<int64_t>(units * tiles, sms));
+  p.status = status;
+  CUtensorMap mk, mv;
+  const int box = std::min(p.page, kTileRows);
+  if ((rc = encode_map(&mk, kc, box)) || (rc = encode_map(&mv, vc, box))) return rc;
+  timing_begin();
+  const size_t n_rows = 2 * static_cast<size_t>(p.blocks) * p.rows_n;
+  const size_t o_bytes = n_rows * p.D * sizeof(float), ml_bytes = n_rows * 2 * sizeof(float);
+  void* scratch = nullptr;
+  if (scratch_alloc(&scratch, o_bytes + ml_bytes + p.blocks * sizeof(int4), st) != cudaSuccess) return FFPA_ERR_CUDA;
+  p.part_o = static_cast<float*>(scratch);
+  p.part_ml = reinterpret_cast<float*>(static_cast<char*>(scratch) + o_bytes);
+  p.starts = reinterpret_cast<int4*>(static_cast<char*>(scratch) + o_bytes + ml_bytes);
+  cudaError_t e = launch_fwd_tree(p, mk, mv, dtype_is_bf16(c.dtype), st);
+  cudaError_t e2 = cudaFreeAsync(scratch, st);
+  return cuda_rc(e != cudaSuccess ? e : e2);
+}
+
+int cache_plan_impl(const int32_t* lens, const int32_t* new_lens, int n_reqs, int page, int32_t* table, int max_pages,
+                    const int32_t* free_pages, int n_free, const int32_t* free_head, int32_t* cu_new, int64_t* slots,
+                    int64_t max_new, int32_t* lens_out, int32_t* free_head_out, ffpa_stream_t stream) {
+  int rc;
+  if ((rc = check_ints(lens, 4, true)) || (rc = check_ints(new_lens, 4, true)) || (rc = check_ints(table, 4, true)) ||
+      (rc = check_ints(free_pages, 4, n_free > 0)) || (rc = check_ints(free_head, 4, true)) ||
+      (rc = check_ints(cu_new, 4, true)) || (rc = check_ints(slots, 8, max_new > 0)) ||
+      (rc = check_ints(lens_out, 4, true)) || (rc = check_ints(free_head_out, 4, true)))
+    return rc;
+  if (n_reqs < 1 || page < 1 || max_pages < 1 || n_free < 0 || max_new < 0) return FFPA_ERR_INVALID_ARG;
+  if (n_reqs > (1 << 20) || max_new > (1ll << 30)) return FFPA_ERR_UNSUPPORTED;
+  PlanParams p = {};
+  p.lens = lens;
+  p.new_lens = new_lens;
+  p.table = table;
+  p.table_stride = max_pages;
+  p.free_pages = free_pages;
+  p.free_head = free_head;
+  p.cu = cu_new;
+  p.slots = slots;
+  p.lens_out = lens_out;
+  p.free_head_out = free_head_out;
+  p.B = n_reqs;
+  p.page = page;
+  p.max_pages = max_pages;
+  p.n_free = n_free;
+  p.max_new = max_new;
+  p.status = device_status_word();
+  if (!p.status) return FFPA_ERR_CUDA;
+  timing_begin();
+  timing_mark(reinterpret_cast<cudaStream_t>(stream));
+  return cuda_rc(launch_cache_plan(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int cache_append_impl(const ffpa_tensor_t* k, const ffpa_tensor_t* v, const ffpa_tensor_t* kc, const ffpa_tensor_t* vc,
+                      const int64_t* slots, ffpa_stream_t stream) {
+  if (!k || !v || !kc || !vc) return FFPA_ERR_INVALID_ARG;
+  if (!is_half_dtype(k->dtype)) return FFPA_ERR_UNSUPPORTED;
+  const int64_t D = k->shape[3];
+  const Shape4 want = {1, kc->shape[1], k->shape[2], D};
+  if (want.H < 1 || want.N < 1 || D < 1) return FFPA_ERR_INVALID_ARG;
+  if (D % 64 != 0 || D > 1024 || want.N > (1ll << 30)) return FFPA_ERR_UNSUPPORTED;
+  int rc;
+  if ((rc = check_bhnd(k, k->dtype, want)) || (rc = check_bhnd(v, k->dtype, want))) return rc;
+  if ((rc = check_caches(kc, vc, k->dtype, D))) return rc;
+  if ((rc = check_ints(slots, 8, true))) return rc;
+  AppendParams p = {};
+  p.k = k->data;
+  p.v = v->data;
+  p.kc = kc->data;
+  p.vc = vc->data;
+  p.k_sh = k->stride[1]; p.k_sn = k->stride[2];
+  p.v_sh = v->stride[1]; p.v_sn = v->stride[2];
+  p.kc_sp = kc->stride[0]; p.kc_sh = kc->stride[1]; p.kc_sn = kc->stride[2];
+  p.vc_sp = vc->stride[0]; p.vc_sh = vc->stride[1]; p.vc_sn = vc->stride[2];
+  p.slots = slots;
+  p.T = want.N;
+  p.H = (int)want.H;
+  p.D = (int)D;
+  p.page = (int)kc->shape[2];
+  p.n_pages = (int)kc->shape[0];
+  p.status = device_status_word();
+  const int sms = device_sm_count();
+  if (!p.status || sms <= 0) return FFPA_ERR_CUDA;
+  timing_begin();
+  timing_mark(reinterpret_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_cache_append(p, sms, reinterpret_cast<cudaStream_t>(stream));
+  timing_mark(reinterpret_cast<cudaStream_t>(stream));
+  return cuda_rc(e);
+}
+
 }  // namespace
 
 extern "C" int ffpa_fwd(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_tensor_t* v,
@@ -686,6 +847,27 @@ extern "C" int ffpa_bwd_varlen(const ffpa_tensor_t* q, const ffpa_tensor_t* k, c
                                const ffpa_tensor_t* dq, const ffpa_tensor_t* dk, const ffpa_tensor_t* dv,
                                ffpa_stream_t stream) {
   return bwd_varlen_impl(q, k, v, cu_seqlens, n_seqs, causal, scale, out, lse, dout, dq, dk, dv, stream);
+}
+
+extern "C" int ffpa_fwd_tree(const ffpa_tensor_t* q, const ffpa_tensor_t* k_cache, const ffpa_tensor_t* v_cache,
+                             const int32_t* block_table, int max_pages, const int32_t* seq_lens,
+                             const int32_t* draft_lens, const uint8_t* tree_mask, int mask_batch, float scale,
+                             const ffpa_tensor_t* out, const ffpa_tensor_t* lse, ffpa_stream_t stream) {
+  return fwd_tree_impl(q, k_cache, v_cache, block_table, max_pages, seq_lens, draft_lens, tree_mask, mask_batch, scale,
+                       out, lse, stream);
+}
+
+extern "C" int ffpa_cache_plan(const int32_t* lens, const int32_t* new_lens, int n_reqs, int page_size,
+                               int32_t* block_table, int max_pages, const int32_t* free_pages, int n_free,
+                               const int32_t* free_head, int32_t* cu_new, int64_t* slots, int64_t max_new,
+                               int32_t* lens_out, int32_t* free_head_out, ffpa_stream_t stream) {
+  return cache_plan_impl(lens, new_lens, n_reqs, page_size, block_table, max_pages, free_pages, n_free, free_head,
+                         cu_new, slots, max_new, lens_out, free_head_out, stream);
+}
+
+extern "C" int ffpa_cache_append(const ffpa_tensor_t* k, const ffpa_tensor_t* v, const ffpa_tensor_t* k_cache,
+                                 const ffpa_tensor_t* v_cache, const int64_t* slots, ffpa_stream_t stream) {
+  return cache_append_impl(k, v, k_cache, v_cache, slots, stream);
 }
 
 // Decode without allocation: validation and parameters as ffpa_fwd's decode

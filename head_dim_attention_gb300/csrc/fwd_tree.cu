@@ -1,0 +1,851 @@
+// Attention of drafted tokens over a paged cache (one token per request is the
+// decode case) on sm_103a.
+//
+// Request b has n = seq_lens[b] tokens in the cache, the last m of them its
+// drafted tokens.  Row i of the m attends to every position before the drafts
+// and, of the drafts, to those its mask row marks (no mask: those up to
+// itself).  Query heads of a GQA group share their kv head's keys, so a kv head
+// of a request has group * m rows.
+//
+// What bounds it: reading K and V once, 4 D bytes per key and kv head.  A tile
+// of 128 query rows would be mostly padding, so the operands are swapped: keys
+// and head-dimension columns are the MMA's M, the rows its N (16, 32 or 64):
+//   S^T [128 keys, N]  = K_tile (K-major A) . Q^T (K-major B)
+//   O^T [128 columns, N] += V_tile^T (MN-major A) . P^T (MN-major B)
+// O^T of all D columns stays in TMEM (ceil(D / 128) N columns of 512), the S^T
+// buffers above it, and the tensor work follows the rows there are.
+//
+// Work is cut evenly, not per request: the 128-key tiles of all (request, kv
+// head, row tile) units form one line, and block c of G takes tiles
+// [W c / G, W (c + 1) / G).  A unit that lies in one block is finished there;
+// one that crosses blocks leaves fp32 partials (O unnormalised, max, sum), at
+// most two per block, and the merge kernel joins them.  Lengths are read on
+// the device only.
+//
+// Pages: a key tile is 128 / page boxes of `page` rows (a page of 128 rows or
+// more is read in boxes of 128).  The box that holds the last valid rows starts
+// earlier by as many rows as it lacks: rows before the page are out of range
+// and arrive as zeros, so nothing behind the length, NaN included, is ever
+// read.  Boxes past the length, and pages with a bad number, use a page index
+// out of range: zeros.  The scores of such rows are -inf.
+//
+// P goes to shared memory as two terms of the input type, the rounded weight
+// and its rounding residual, each with its own product: the matrix pipe has
+// the time, and O then carries P to about 2^-16.
+//
+// Warps: 0 and 2 TMA producers (alternate ring slots; the lanes of a warp issue
+// a slot's boxes), 1 TMEM owner and MMA issuer, from 4 on softmax, correction
+// and epilogue: one warpgroup for N <= 32, two for N = 64 (32 rows each; thread
+// = key of S^T, then column of O^T).  Every wait is bounded.
+#include <algorithm>
+#include <type_traits>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace ffpa {
+namespace {
+
+constexpr int kSlotBytes = 2 * kChunkBytes;  // two 64-column chunks of 128 keys
+constexpr int kPBytes = kTileRows * 128;     // 128 keys x 64 rows of 16 bits
+constexpr int kMaxSlots = 6;
+constexpr int kMaxSmem = 232448;
+constexpr float kRescaleLog2 = 8.0f;  // rescale O only when a row's max grows by > 2^8
+// The largest weight of a row is 2^kTop when its reference is set: fp16 ends at
+// 2^16 above and, in steps of 2^-24, below, so its weights are moved up by 2^6
+// (at most 2^14 before the next rescale); bf16 has fp32's range.
+template <bool BF16>
+constexpr float kTop = BF16 ? 0.f : 6.f;
+constexpr int kMergeThreads = 128;
+
+// One request as the device sees it: n cached tokens, the last m of them drafts.
+struct Request {
+  int n, m;
+};
+
+__device__ __forceinline__ Request request(const TreeParams& p, int b) {
+  Request r;
+  r.n = __ldg(p.seq_lens + b);
+  r.m = p.draft_lens ? __ldg(p.draft_lens + b) : p.T;
+  const int cap = p.max_pages * p.page;
+  if (r.n < 0 || r.n > cap || r.m < 0 || r.m > p.T || (r.m > r.n && (r.n > 0 || p.draft_lens))) {
+    record_error(p.status, FFPA_DEV_LENGTHS);
+    r.n = max(0, min(r.n, cap));
+    r.m = max(0, min(r.m, p.T));
+  }
+  r.m = min(r.m, r.n);  // an empty entry of a padded batch: no rows
+  return r;
+}
+template <int N>
+__device__ __forceinline__ int row_tiles(const TreeParams& p, const Request& r) {
+  return (p.group * r.m + N - 1) / N;
+}
+__device__ __forceinline__ int key_tiles(const Request& r) { return r.m > 0 ? (r.n + kTileRows - 1) / kTileRows : 0; }
+template <int N>
+__device__ __forceinline__ int64_t request_work(const TreeParams& p, const Request& r) {
+  return static_cast<int64_t>(p.Hkv) * row_tiles<N>(p, r) * key_tiles(r);
+}
+
+// The requests' work, all of it and before the run of requests that this thread
+// takes; `sums` has threads / 32 entries.
+struct WorkSum {
+  int64_t before_run, run, total;
+  int first, last;  // requests of this thread's run
+};
+template <int N>
+__device__ __forceinline__ WorkSum sum_work(const TreeParams& p, int64_t* sums, int threads) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = (p.B + threads - 1) / threads;
+  WorkSum w;
+  w.first = min(p.B, tid * per);
+  w.last = min(p.B, w.first + per);
+  w.run = 0;
+  for (int b = w.first; b < w.last; ++b) w.run += request_work<N>(p, request(p, b));
+  int64_t incl = w.run;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  w.before_run = incl - w.run;
+  w.total = 0;
+  for (int i = 0; i < threads / 32; ++i) {
+    if (i < warp) w.before_run += sums[i];
+    w.total += sums[i];
+  }
+  return w;
+}
+
+// First tile of block c of `blocks`.
+__device__ __forceinline__ int64_t block_start(int64_t total, int blocks, int c) { return total * c / blocks; }
+
+// The units of one block, in order.  Every role walks its own copy.
+template <int N>
+struct Walk {
+  int64_t left;        // tiles of the line still to take
+  int b, sub;          // request; kv head * row tiles + row tile
+  int tile;            // first key tile of the current segment
+  Request r;
+  int rt, tiles;       // row tiles per kv head and key tiles of the request
+  int hk, row0;        // kv head, first row of the row tile
+  int end;             // one past the segment's last key tile
+
+  __device__ __forceinline__ void load(const TreeParams& p) {
+    r = request(p, b);
+    rt = row_tiles<N>(p, r);
+    tiles = key_tiles(r);
+  }
+  __device__ __forceinline__ void place() {
+    hk = sub / rt;
+    row0 = (sub % rt) * N;
+    end = static_cast<int>(min(static_cast<int64_t>(tiles), tile + left));
+  }
+  // `offset`: the block's first tile within request b0's work
+  __device__ __forceinline__ void begin(const TreeParams& p, int b0, int64_t offset, int64_t count) {
+    left = count;
+    b = b0;
+    load(p);
+    sub = static_cast<int>(offset / tiles);
+    tile = static_cast<int>(offset % tiles);
+    place();
+  }
+  // to the next segment; false when the block's tiles are used up
+  __device__ __forceinline__ bool next(const TreeParams& p) {
+    left -= end - tile;
+    if (left <= 0) return false;
+    tile = 0;
+    if (++sub == rt * p.Hkv) {
+      sub = 0;
+      do {
+        ++b;
+        if (b >= p.B) return false;
+        load(p);
+      } while (tiles == 0 || rt == 0);
+    }
+    place();
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return tile == 0 && end == tiles; }
+};
+
+struct Bars {
+  int full, empty, q_full, s_full, s_free, p_ready, pv_done, o_free, drain, count;
+};
+__host__ __device__ constexpr Bars bar_layout() {
+  return Bars{0, kMaxSlots, 2 * kMaxSlots, 2 * kMaxSlots + 1, 2 * kMaxSlots + 3, 2 * kMaxSlots + 5,
+              2 * kMaxSlots + 6, 2 * kMaxSlots + 7, 2 * kMaxSlots + 8, 2 * kMaxSlots + 9};
+}
+
+constexpr int kMiscBytes = 256 /* barriers, TMEM base, start */ + 8 * 128 /* work sums */ + 128 * 8 /* vis */ +
+                           64 * 8 * 2 /* rows in out and lse */ + 12 * 32 * 4 * 2 /* statistics */;
+__host__ __device__ constexpr int q_bytes(int n_chunks, int N) { return n_chunks * N * 128; }
+__host__ __device__ constexpr int fixed_bytes(int n_chunks, int N) {
+  return q_bytes(n_chunks, N) + 2 * kPBytes + kMiscBytes + 1024;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (BF16) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+  } else {
+    __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (BF16)
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+  else
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <bool BF16>
+__device__ __forceinline__ void store1(void* base, int64_t at, float x) {
+  if constexpr (BF16)
+    static_cast<__nv_bfloat16*>(base)[at] = __float2bfloat16_rn(x);
+  else
+    static_cast<__half*>(base)[at] = __float2half_rn(x);
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// All `threads` threads meet; true if every one of them passes true.
+__device__ __forceinline__ bool bar_and(uint32_t id, uint32_t threads, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// C consecutive TMEM columns of this thread's lane (C = 16 or 32)
+template <int C>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[C]) {
+  if constexpr (C == 32)
+    tmem_ld32(taddr, r);
+  else
+    tmem_ld16(taddr, r);
+  tmem_ld_wait();
+}
+template <int C>
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[C]) {
+  if constexpr (C == 32)
+    tmem_st32(taddr, r);
+  else
+    tmem_st16(taddr, r);
+}
+
+struct MaxOp {
+  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct SumOp {
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+// Reduces each of the C columns over the 32 lanes; lane l returns column l mod
+// C.  At every step a lane keeps half of its columns and trades the others with
+// the lane that keeps those: 31 exchanges for all C columns.
+template <int C, class Op>
+__device__ __forceinline__ float reduce_columns(float (&v)[C], int lane, Op op) {
+  if constexpr (C == 16) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = op(v[i], __shfl_xor_sync(0xffffffffu, v[i], 16));
+  }
+#pragma unroll
+  for (int h = (C == 32 ? 16 : 8); h >= 1; h >>= 1) {
+    const bool up = (lane & h) != 0;
+#pragma unroll
+    for (int i = 0; i < h; ++i) {
+      const float send = up ? v[i] : v[i + h], keep = up ? v[i + h] : v[i];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, h));
+    }
+  }
+  return v[0];
+}
+
+template <int N>
+constexpr int tree_threads() {
+  return N == 64 ? 384 : 256;
+}
+
+template <int N, bool BF16>
+__global__ void __launch_bounds__(tree_threads<N>(), 1)
+    tree_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                const __grid_constant__ TreeParams p) {
+  typedef typename std::conditional<BF16, __nv_bfloat16, __half>::type T;
+  constexpr int kThreads = tree_threads<N>();
+  constexpr int kSoftWarps = kThreads / 32 - 4;
+  constexpr int C = N == 64 ? 32 : N;  // rows per softmax thread
+  constexpr Bars bl = bar_layout();
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int NC = p.n_chunks, slots = p.slots;
+  const uint32_t ring = smem_u32(smem), p_hi = ring + slots * kSlotBytes, p_lo = p_hi + kPBytes;
+  const uint32_t q_sm = p_lo + kPBytes;
+  uint8_t* misc = smem + slots * kSlotBytes + 2 * kPBytes + q_bytes(NC, N);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(misc);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + bl.count);
+  int64_t* start = reinterpret_cast<int64_t*>(misc + 232);  // [3]: request, offset in its work, tiles of this block
+  int64_t* sums = reinterpret_cast<int64_t*>(misc + 256);
+  uint64_t* vis = reinterpret_cast<uint64_t*>(misc + 256 + 1024);      // [128] draft -> rows that see it
+  int64_t* row_off = reinterpret_cast<int64_t*>(vis + 128);            // [N] offset of the row in out, -1: padding
+  int64_t* row_lse = row_off + 64;                                     // [N] index of the row in lse
+  float* stat = reinterpret_cast<float*>(row_lse + 64);                // [warps][32] exchanged statistics
+  float* bcast = stat + 12 * 32;                                       // [warps][32] per-row values of one warp
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+  static_assert(bl.count * 8 + 8 <= 232, "barrier area");
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t* status = p.status;
+  if (tid == 0) {
+    for (int i = 0; i < slots; ++i) {
+      mbar_init(bar(bl.full + i), 1);
+      mbar_init(bar(bl.empty + i), 1);
+    }
+    mbar_init(bar(bl.q_full), kSoftWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(bl.s_full + i), 1);
+      mbar_init(bar(bl.s_free + i), kSoftWarps);
+    }
+    mbar_init(bar(bl.p_ready), kSoftWarps);
+    mbar_init(bar(bl.pv_done), 1);
+    mbar_init(bar(bl.o_free), kSoftWarps);
+    mbar_init(bar(bl.drain), 1);
+    fence_mbar_init();
+    start[2] = 0;
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  {
+    const WorkSum w = sum_work<N>(p, sums, kThreads);  // contains a __syncthreads
+    if (w.total > 0) {
+      const int blocks = static_cast<int>(min(static_cast<int64_t>(gridDim.x), w.total));
+      const int c = blockIdx.x;
+      if (c < blocks) {
+        const int64_t w0 = block_start(w.total, blocks, c), w1 = block_start(w.total, blocks, c + 1);
+        if (w0 >= w.before_run && w0 < w.before_run + w.run) {
+          int64_t at = w.before_run;
+          for (int b = w.first; b < w.last; ++b) {
+            const int64_t x = request_work<N>(p, request(p, b));
+            if (w0 < at + x) {
+              start[0] = b;
+              start[1] = w0 - at;
+              start[2] = w1 - w0;
+              break;
+            }
+            at += x;
+          }
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    // where this block starts, for the merge kernel
+    int4 at = make_int4(-1, 0, 0, 0);
+    if (start[2] > 0) {
+      Walk<N> w;
+      w.begin(p, static_cast<int>(start[0]), start[1], start[2]);
+      at = make_int4(w.b, w.sub, w.tile, 0);
+    }
+    p.starts[blockIdx.x] = at;
+  }
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+  const bool any = start[2] > 0;
+  const uint32_t s_tm = 512 - 2 * N;  // the two S^T buffers above O^T
+  const int kslots = (NC + 1) / 2;    // ring slots of one key tile of K, or of V
+
+  if (any && (warp == 0 || warp == 2)) {
+    // ------------------------------------------------------------ TMA producers
+    // Loads in the order of use: K of tile 0; then K of tile t + 1, V of tile t.
+    // Warp 0 takes the even loads, warp 2 the odd ones (two slots at least, so
+    // neither runs a round ahead of a slot's barrier).
+    const int pi = warp >> 1;
+    const int box = min(p.page, kTileRows), pieces = kTileRows / box;
+    if (lane == 0) {
+      tma_prefetch_desc(&map_k);
+      tma_prefetch_desc(&map_v);
+    }
+    bool ok = true;
+    uint32_t it = 0;
+    // one key tile of K or V: lane l issues box l of each slot (piece l mod pieces, chunk l / pieces)
+    auto load_tile = [&](const CUtensorMap* m, const Walk<N>& w, int t) {
+      const int piece = lane % pieces, ch = lane / pieces;
+      const int pos = t * kTileRows + piece * box;  // first position of the box
+      int row = 0, page = p.n_pages;                // out of range: zeros
+      if (ch < 2 && pos < w.r.n) {
+        page = __ldg(p.table + static_cast<int64_t>(w.b) * p.table_stride + pos / p.page);
+        if (page < 0 || page >= p.n_pages) {
+          record_error(status, FFPA_DEV_LENGTHS);
+          page = p.n_pages;
+        }
+        row = pos % p.page + min(0, w.r.n - pos - box);  // the last box ends at the last valid row
+      }
+      for (int s2 = 0; s2 < kslots && ok; ++s2, ++it) {
+        if (static_cast<int>(it & 1) != pi) continue;
+        const uint32_t s = it % slots, rd = it / slots;
+        ok = mbar_wait<false>(bar(bl.empty + s), (rd & 1) ^ 1, status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const int cn = min(2, NC - 2 * s2);
+        if (lane == 0) mbar_expect_tx(bar(bl.full + s), cn * kChunkBytes);
+        __syncwarp();
+        if (ch < cn)
+          tma_load_4d(ring + s * kSlotBytes + ch * kChunkBytes + piece * box * 128, m, bar(bl.full + s),
+                      (2 * s2 + ch) * kChunk, row, w.hk, page);
+      }
+    };
+    Walk<N> w;
+    w.begin(p, static_cast<int>(start[0]), start[1], start[2]);
+    do {
+      load_tile(&map_k, w, w.tile);
+      for (int t = w.tile; t < w.end && ok; ++t) {
+        if (t + 1 < w.end) load_tile(&map_k, w, t + 1);
+        load_tile(&map_v, w, t);
+      }
+    } while (ok && w.next(p));
+    // the last release of every slot this warp loaded last (commit arrivals are
+    // not ordered with one another and must not land after the block is gone)
+    if (lane == 0)
+      for (uint32_t s = 0; s < static_cast<uint32_t>(slots) && s < it && ok; ++s) {
+        const uint32_t last = s + ((it - 1 - s) / slots) * slots;
+        if (static_cast<int>(last & 1) == pi) mbar_wait<false>(bar(bl.empty + s), (last / slots) & 1, status);
+      }
+  } else if (any && warp == 1 && lane == 0) {
+    // ------------------------------------------------------------ MMA issuer
+    constexpr uint32_t idesc_s = idesc_f16(BF16, 128, N, false, false);
+    constexpr uint32_t idesc_o = idesc_f16(BF16, 128, N, true, true);
+    const uint64_t dk = sdesc_sw128(ring, 16, 1024), dv = sdesc_sw128(ring, kChunkBytes, 1024);
+    const uint64_t dq = sdesc_sw128(q_sm, 16, 1024);
+    const uint64_t dhi = sdesc_sw128(p_hi, 16, 1024), dlo = sdesc_sw128(p_lo, 16, 1024);
+    bool ok = true;
+    uint32_t it = 0, tc = 0, unit = 0;  // ring loads, S^T tiles and units so far
+    auto scores = [&]() {
+      if (tc >= 2) {
+        ok = mbar_wait<false>(bar(bl.s_free + (tc & 1)), ((tc - 2) >> 1) & 1, status);
+        if (!ok) return;
+        tc_fence_after();
+      }
+      const uint32_t d = tbase + s_tm + (tc & 1) * N;
+      for (int s2 = 0; s2 < kslots; ++s2, ++it) {
+        const uint32_t s = it % slots;
+        ok = mbar_wait<false>(bar(bl.full + s), (it / slots) & 1, status);
+        if (!ok) return;
+        tc_fence_after();
+        const int cn = min(2, NC - 2 * s2);
+        for (int i = 0; i < cn; ++i) {
+          const uint64_t a = sdesc_advance(dk, s * kSlotBytes + i * kChunkBytes);
+          const uint64_t b = sdesc_advance(dq, (2 * s2 + i) * N * 128);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_ss(d, sdesc_advance(a, kk * 32), sdesc_advance(b, kk * 32), idesc_s, (s2 | i | kk) != 0);
+        }
+        umma_commit(bar(bl.empty + s));
+      }
+      umma_commit(bar(bl.s_full + (tc & 1)));
+      ++tc;
+    };
+    Walk<N> w;
+    w.begin(p, static_cast<int>(start[0]), start[1], start[2]);
+    uint32_t pv = 0;  // P V products so far
+    do {
+      ok = mbar_wait<false>(bar(bl.q_full), unit & 1, status);
+      if (!ok) break;
+      tc_fence_after();
+      scores();
+      for (int t = w.tile; t < w.end && ok; ++t, ++pv) {
+        if (t + 1 < w.end) scores();
+        if (!ok) break;
+        if (t == w.tile && unit > 0) {  // the epilogue of the unit before has read O^T
+          ok = mbar_wait<false>(bar(bl.o_free), (unit - 1) & 1, status);
+          if (!ok) break;
+        }
+        ok = mbar_wait<false>(bar(bl.p_ready), pv & 1, status);
+        if (!ok) break;
+        tc_fence_after();
+        for (int s2 = 0; s2 < kslots && ok; ++s2, ++it) {
+          const uint32_t s = it % slots;
+          ok = mbar_wait<false>(bar(bl.full + s), (it / slots) & 1, status);
+          if (!ok) break;
+          tc_fence_after();
+          // columns 128 s2 .. of O^T; at an odd chunk count the last slot's second
+          // half is stale shared memory: it reaches only O^T rows past D
+          const uint64_t a = sdesc_advance(dv, s * kSlotBytes);
+          const uint32_t d = tbase + s2 * N;
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            umma_ss(d, sdesc_advance(a, ks * 2048), sdesc_advance(dhi, ks * 2048), idesc_o, t > w.tile || ks > 0);
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            umma_ss(d, sdesc_advance(a, ks * 2048), sdesc_advance(dlo, ks * 2048), idesc_o, 1u);
+          umma_commit(bar(bl.empty + s));
+        }
+        if (!ok) break;
+        umma_commit(bar(bl.pv_done));
+      }
+      ++unit;
+    } while (ok && w.next(p));
+    umma_commit(bar(bl.drain));
+    mbar_wait<false>(bar(bl.drain), 0, status);
+  } else if (any && warp >= 4) {
+    // ------------------------------------------------------------ softmax / correction / epilogue
+    const int st = tid - 128;           // softmax thread
+    const int wg = st >> 7;             // its rows: C wg .. C wg + C - 1 of the row tile
+    const int t = st & 127;             // TMEM lane: key of S^T, column of O^T
+    const int sw = warp - 4;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t nb = 1 + wg;         // named barrier of this warpgroup
+    constexpr uint32_t kAll = kSoftWarps * 32;
+    float* my_stat = stat + sw * 32;
+    float* my_bcast = bcast + sw * 32;
+    const float* wg_stat = stat + wg * 4 * 32;
+    const int box = min(p.page, kTileRows);
+    constexpr float kLn2 = 0.6931471805599453f;
+    bool ok = true;
+    uint32_t tc = 0;
+    Walk<N> w;
+    w.begin(p, static_cast<int>(start[0]), start[1], start[2]);
+    do {
+      const int m = w.r.m, n = w.r.n, prefix = n - m, rows = p.group * m;
+      // ---- the unit: row offsets, draft visibility, Q
+      if (!bar_and(3, kAll, ok)) break;  // the epilogue before has read the tables
+      if (st < N) {
+        const int rr = w.row0 + st;
+        int64_t off = -1;
+        int64_t li = 0;
+        if (rr < rows) {
+          const int h = w.hk * p.group + rr / m, i = rr % m;
+          off = w.b * p.o_sb + h * p.o_sh + i * p.o_sn;
+          li = (static_cast<int64_t>(w.b) * p.Hq + h) * p.T + i;
+        }
+        row_off[st] = off;
+        row_lse[st] = li;
+      }
+      if (w.end * kTileRows > prefix) {  // this segment has drafts among its keys
+        for (int j = st; j < m; j += kAll) {
+          uint64_t bits = 0;
+          for (int x = 0; x < N; ++x) {
+            const int rr = w.row0 + x;
+            if (rr >= rows) break;
+            const int i = rr % m;
+            const bool see = p.mask ? __ldg(p.mask + w.b * p.mask_sb + static_cast<int64_t>(i) * p.T + j) != 0 : j <= i;
+            if (see) bits |= 1ull << x;
+          }
+          vis[j] = bits;
+        }
+      }
+      // Q rows of the tile, K-major with the 128-byte swizzle; padding rows zero
+      const int vecs = N * NC * 8;  // 16-byte pieces: piece v is row v / (8 NC), granule v % (8 NC)
+      for (int v0 = st; v0 < vecs; v0 += 8 * kAll) {
+        uint4 x[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int v = v0 + u * kAll, rr = w.row0 + v / (8 * NC), gq = v % (8 * NC);
+          x[u] = make_uint4(0u, 0u, 0u, 0u);
+          if (v < vecs && rr < rows)
+            x[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + w.b * p.q_sb +
+                                                        (w.hk * p.group + rr / m) * p.q_sh + (rr % m) * p.q_sn) +
+                         gq);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int v = v0 + u * kAll, r = v / (8 * NC), gq = v % (8 * NC);
+          if (v < vecs)
+            st_shared_v4(q_sm + (gq >> 3) * (N * 128) + r * 128 + (((gq & 7) ^ (r & 7)) << 4), x[u].x, x[u].y, x[u].z,
+                         x[u].w);
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bl.q_full));
+      if (!bar_and(3, kAll, ok)) break;  // tables written
+
+      float l[C];  // this key's share of the rows' sums
+#pragma unroll
+      for (int x = 0; x < C; ++x) l[x] = 0.f;
+      float m_used = -INFINITY;  // lane x mod C: reference maximum of row x (log2 domain), the same in all warps
+      for (int tile = w.tile; tile < w.end; ++tile, ++tc) {
+        if (ok) ok = mbar_wait<false>(bar(bl.s_full + (tc & 1)), (tc >> 1) & 1, status);
+        ok = __all_sync(0xffffffffu, ok);
+        float s[C];
+        if (ok) {
+          tc_fence_after();
+          uint32_t v[C];
+          tmem_load<C>(tbase + lane_off + s_tm + (tc & 1) * N + wg * C, v);
+#pragma unroll
+          for (int x = 0; x < C; ++x) s[x] = __uint_as_float(v[x]);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(bl.s_free + (tc & 1)));
+        } else {
+#pragma unroll
+          for (int x = 0; x < C; ++x) s[x] = 0.f;
+        }
+        if ((tile + 1) * kTileRows > prefix) {
+          // position of this thread's key: a box that the length cuts ends at the last valid row
+          const int r = t % box, base = tile * kTileRows + t - r;
+          const int shift = max(0, base + box - n);
+          const int pos = base + r - shift;
+          uint32_t see = 0xffffffffu;
+          if (r < shift)
+            see = 0u;
+          else if (pos >= prefix)
+            see = static_cast<uint32_t>(vis[pos - prefix] >> (wg * C));
+#pragma unroll
+          for (int x = 0; x < C; ++x)
+            if (!((see >> x) & 1u)) s[x] = -INFINITY;
+        }
+        // row maxima: over the warp's 32 keys, then over the four warps
+        {
+          float mx[C];
+#pragma unroll
+          for (int x = 0; x < C; ++x) mx[x] = s[x];
+          my_stat[lane] = reduce_columns<C>(mx, lane, MaxOp()) * p.scale_log2;
+        }
+        // A warp that gave up on a wait keeps taking part in the barriers: all
+        // softmax warps leave together at the next unit.
+        ok = bar_and(nb, 128, ok);
+        float alpha = 1.f;
+        {
+          const float m_tile = fmaxf(fmaxf(wg_stat[lane], wg_stat[32 + lane]), fmaxf(wg_stat[64 + lane], wg_stat[96 + lane]));
+          if (m_used == -INFINITY) {
+            m_used = m_tile - kTop<BF16>;
+          } else if (m_tile - kTop<BF16> > m_used + kRescaleLog2) {
+            alpha = ex2(m_used - (m_tile - kTop<BF16>));
+            m_used = m_tile - kTop<BF16>;
+          }
+          my_bcast[lane] = m_used == -INFINITY ? 0.f : m_used;
+          __syncwarp();
+        }
+        // P (and its rounding residual) of this key
+        uint32_t hi[C / 2], lo[C / 2];
+        const bool rescale = __any_sync(0xffffffffu, alpha != 1.f);  // the same in the four warps
+        if (rescale) {
+#pragma unroll
+          for (int x = 0; x < C; ++x) l[x] *= __shfl_sync(0xffffffffu, alpha, x);
+        }
+#pragma unroll
+        for (int x = 0; x < C; x += 4) {
+          const float4 ref = *reinterpret_cast<const float4*>(my_bcast + x);
+          const float p0 = ex2(fmaf(s[x], p.scale_log2, -ref.x)), p1 = ex2(fmaf(s[x + 1], p.scale_log2, -ref.y));
+          const float p2 = ex2(fmaf(s[x + 2], p.scale_log2, -ref.z)), p3 = ex2(fmaf(s[x + 3], p.scale_log2, -ref.w));
+          l[x] += p0;
+          l[x + 1] += p1;
+          l[x + 2] += p2;
+          l[x + 3] += p3;
+          hi[x / 2] = pack2<BF16>(p0, p1);
+          hi[x / 2 + 1] = pack2<BF16>(p2, p3);
+          const float2 a = unpack2<BF16>(hi[x / 2]), b = unpack2<BF16>(hi[x / 2 + 1]);
+          lo[x / 2] = pack2<BF16>(p0 - a.x, p1 - a.y);
+          lo[x / 2 + 1] = pack2<BF16>(p2 - b.x, p3 - b.y);
+        }
+        if (tc > 0) {  // the product before has read P and written O^T
+          if (ok) ok = mbar_wait<false>(bar(bl.pv_done), (tc - 1) & 1, status);
+          ok = __all_sync(0xffffffffu, ok);
+        }
+        if (rescale && tile > w.tile && ok) {
+          tc_fence_after();
+          for (int blk = 0; blk < kslots; ++blk) {
+            uint32_t v[C];
+            const uint32_t a = tbase + lane_off + blk * N + wg * C;
+            tmem_load<C>(a, v);
+#pragma unroll
+            for (int x = 0; x < C; ++x)
+              v[x] = __float_as_uint(__uint_as_float(v[x]) * __shfl_sync(0xffffffffu, alpha, x));
+            tmem_store<C>(a, v);
+          }
+          tmem_st_wait();
+        }
+        {
+          const uint32_t row = static_cast<uint32_t>(t) * 128u;
+#pragma unroll
+          for (int g = 0; g < C / 8; ++g) {
+            const uint32_t at = row + (static_cast<uint32_t>((wg * (C / 8) + g) ^ (t & 7)) << 4);
+            st_shared_v4(p_hi + at, hi[4 * g], hi[4 * g + 1], hi[4 * g + 2], hi[4 * g + 3]);
+            st_shared_v4(p_lo + at, lo[4 * g], lo[4 * g + 1], lo[4 * g + 2], lo[4 * g + 3]);
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bl.p_ready));
+      }
+      // ---- the unit's end: row sums, then O^T to out or to a partial
+      if (ok) ok = mbar_wait<false>(bar(bl.pv_done), (tc - 1) & 1, status);
+      ok = __all_sync(0xffffffffu, ok);
+      my_stat[lane] = reduce_columns<C>(l, lane, SumOp());
+      ok = bar_and(nb, 128, ok);
+      const float sum = (wg_stat[lane] + wg_stat[32 + lane]) + (wg_stat[64 + lane] + wg_stat[96 + lane]);
+      tc_fence_after();
+      if (w.whole()) {
+        my_bcast[lane] = sum > 0.f ? 1.f / sum : 0.f;
+        __syncwarp();
+        for (int blk = 0; blk < kslots; ++blk) {
+          uint32_t v[C];
+          tmem_load<C>(tbase + lane_off + blk * N + wg * C, v);
+          const int d = blk * 128 + t;
+          if (d < p.D) {
+#pragma unroll
+            for (int x = 0; x < C; ++x) {
+              const int64_t off = row_off[wg * C + x];
+              if (off >= 0) store1<BF16>(p.out, off + d, __uint_as_float(v[x]) * my_bcast[x]);
+            }
+          }
+        }
+        if ((warp & 3) == 0 && lane < C && p.lse && row_off[wg * C + lane] >= 0)
+          p.lse[row_lse[wg * C + lane]] = sum > 0.f ? (m_used + __log2f(sum)) * kLn2 : -INFINITY;
+      } else {
+        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (w.tile > 0 ? 0 : 1);
+        for (int blk = 0; blk < kslots; ++blk) {
+          uint32_t v[C];
+          tmem_load<C>(tbase + lane_off + blk * N + wg * C, v);
+          const int d = blk * 128 + t;
+          if (d < p.D) {
+#pragma unroll
+            for (int x = 0; x < C; ++x)
+              if (row_off[wg * C + x] >= 0) p.part_o[(slot * N + wg * C + x) * p.D + d] = __uint_as_float(v[x]);
+          }
+        }
+        if ((warp & 3) == 0 && lane < C) {
+          float* ml = p.part_ml + (slot * N + wg * C + lane) * 2;
+          ml[0] = m_used;
+          ml[1] = sum;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bl.o_free));
+    } while (w.next(p));
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+// Joins the partials of the units that cross blocks.  Block (c, x) looks at the
+// place where attention block c starts: if that is inside a unit, and the
+// first such place in it, it merges row x of the unit.  The unit's first piece
+// is slot 1 of block c - 1, the others slot 0 of the blocks from c on.
+//   O = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c
+template <int N, bool BF16>
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x + 1, x = blockIdx.y;
+  const int4 at = p.starts[c], prev = p.starts[c - 1];
+  if (at.x < 0 || at.z == 0) return;                                  // idle, or at a unit's start
+  if (prev.x == at.x && prev.y == at.y && prev.z > 0) return;         // not the first
+  const int b = at.x, sub = at.y;
+  const Request r = request(p, b);
+  const int rt = row_tiles<N>(p, r);
+  const int rr = (sub % rt) * N + x;
+  if (rr >= p.group * r.m) return;
+  const int h = (sub / rt) * p.group + rr / r.m, i = rr % r.m;
+  int pieces = 2;
+  while (c + pieces - 1 < p.blocks) {
+    const int4 n = p.starts[c + pieces - 1];
+    if (n.x != b || n.y != sub || n.z == 0) break;
+    ++pieces;
+  }
+  auto slot = [&](int k) { return (2 * static_cast<int64_t>(c - 1 + k) + (k == 0 ? 1 : 0)) * N + x; };
+  float M = -INFINITY;
+  for (int k = 0; k < pieces; ++k) M = fmaxf(M, p.part_ml[2 * slot(k)]);
+  const float ref = M == -INFINITY ? 0.f : M;
+  float sum = 0.f;
+  for (int k = 0; k < pieces; ++k) sum += ex2(p.part_ml[2 * slot(k)] - ref) * p.part_ml[2 * slot(k) + 1];
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  typedef typename std::conditional<BF16, __nv_bfloat16, __half>::type T;
+  T* orow = static_cast<T*>(p.out) + b * p.o_sb + h * p.o_sh + i * p.o_sn;
+  for (int d = threadIdx.x * 4; d < p.D; d += kMergeThreads * 4) {
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < pieces; ++k) {
+      const float f = ex2(p.part_ml[2 * slot(k)] - ref);
+      const float4 v = *reinterpret_cast<const float4*>(p.part_o + slot(k) * p.D + d);
+      o.x = fmaf(f, v.x, o.x);
+      o.y = fmaf(f, v.y, o.y);
+      o.z = fmaf(f, v.z, o.z);
+      o.w = fmaf(f, v.w, o.w);
+    }
+    uint2 w;
+    w.x = pack2<BF16>(o.x * inv, o.y * inv);
+    w.y = pack2<BF16>(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2*>(orow + d) = w;
+  }
+  constexpr float kLn2 = 0.6931471805599453f;
+  if (threadIdx.x == 0 && p.lse)
+    p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.T + i] = sum > 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
+}
+
+template <int N, bool BF16>
+cudaError_t launch_n(const TreeParams& p_in, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
+  TreeParams p = p_in;
+  p.slots = std::min(kMaxSlots, (kMaxSmem - fixed_bytes(p.n_chunks, N)) / kSlotBytes);
+  if (p.slots < 2) return cudaErrorInvalidConfiguration;
+  const int smem = fixed_bytes(p.n_chunks, N) + p.slots * kSlotBytes;
+  auto kern = tree_kernel<N, BF16>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  timing_mark(st);
+  kern<<<p.blocks, tree_threads<N>(), smem, st>>>(mk, mv, p);
+  timing_mark(st);
+  if ((e = cudaGetLastError()) != cudaSuccess || p.blocks < 2) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.blocks - 1, N, 1);
+  cfg.blockDim = dim3(kMergeThreads, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, tree_merge_kernel<N, BF16>, p);
+  timing_mark(st);
+  return e;
+}
+
+template <bool BF16>
+cudaError_t launch_tree(const TreeParams& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
+  switch (p.rows_n) {
+    case 16: return launch_n<16, BF16>(p, mk, mv, st);
+    case 32: return launch_n<32, BF16>(p, mk, mv, st);
+    default: return launch_n<64, BF16>(p, mk, mv, st);
+  }
+}
+
+}  // namespace
+
+// Rows per tile: the fewest row tiles, then the smallest N.  O^T takes
+// ceil(D / 128) N columns of TMEM next to 2 N for the scores, so N = 64 serves
+// D <= 768.
+int tree_rows_n(int rows, int D) {
+  const int widest = D <= 768 ? 64 : 32;
+  for (int n = 16; n < widest; n *= 2)
+    if (rows <= n) return n;
+  return widest;
+}
+
+cudaError_t launch_fwd_tree(const TreeParams& p, const CUtensorMap& mk, const CUtensorMap& mv, bool bf16,
+                            cudaStream_t s) {
+  return bf16 ? launch_tree<true>(p, mk, mv, s) : launch_tree<false>(p, mk, mv, s);
+}
+
+}  // namespace ffpa

@@ -104,6 +104,66 @@ struct DecodeParams {
   uint32_t* status;   // device status word (bounded waits of the streaming kernel)
 };
 
+// Drafted tokens over a paged cache (fwd_tree.cu).
+struct TreeParams {
+  const void* q;              // [B, Hq, T, D]
+  void* out;                  // [B, Hq, T, D]
+  float* lse;                 // nullable, contiguous [B, Hq, T]
+  int64_t q_sb, q_sh, q_sn;
+  int64_t o_sb, o_sh, o_sn;
+  const int32_t* table;       // [B, max_pages] page numbers
+  int64_t table_stride;       // between requests
+  const int32_t* seq_lens;    // [B]
+  const int32_t* draft_lens;  // nullable [B]
+  const uint8_t* mask;        // nullable [B or 1, T, T]
+  int64_t mask_sb;            // between requests (0: one mask for all)
+  int B, Hq, Hkv, T, D;
+  int group, n_chunks;
+  int page, n_pages, max_pages;
+  float scale_log2;
+  int rows_n;                 // rows of one row tile: the MMA N
+  int slots;                  // ring slots
+  int blocks;                 // blocks of the attention kernel
+  float* part_o;              // [2 blocks, rows_n, D] fp32 partials
+  float* part_ml;             // [2 blocks, rows_n, 2] their (max, sum), log2 domain
+  int4* starts;               // [blocks] (request or -1, kv head x row tiles + row tile, key tile, 0)
+  uint32_t* status;
+};
+int tree_rows_n(int rows, int D);
+cudaError_t launch_fwd_tree(const TreeParams& p, const CUtensorMap& mk, const CUtensorMap& mv, bool bf16,
+                            cudaStream_t s);
+
+// Paged cache: block tables and slots from request lengths, and writes (cache.cu).
+struct PlanParams {
+  const int32_t* lens;       // [B] tokens in the cache
+  const int32_t* new_lens;   // [B] tokens to add
+  int32_t* table;            // [B, max_pages]
+  int64_t table_stride;
+  const int32_t* free_pages; // [n_free]
+  const int32_t* free_head;  // [1] first page of the list still free
+  int32_t* cu;               // [B + 1] starts of the requests' new tokens
+  int64_t* slots;            // [max_new]
+  int32_t* lens_out;         // [B]
+  int32_t* free_head_out;    // [1]
+  int B, page, max_pages, n_free;
+  int64_t max_new;
+  uint32_t* status;
+};
+cudaError_t launch_cache_plan(const PlanParams& p, cudaStream_t s);
+struct AppendParams {
+  const void* k;             // [1, H, T, D]
+  const void* v;
+  void* kc;                  // [pages, H, page, D]
+  void* vc;
+  int64_t k_sh, k_sn, v_sh, v_sn;
+  int64_t kc_sp, kc_sh, kc_sn, vc_sp, vc_sh, vc_sn;
+  const int64_t* slots;      // [T]
+  int64_t T;
+  int H, D, page, n_pages;
+  uint32_t* status;
+};
+cudaError_t launch_cache_append(const AppendParams& p, int sms, cudaStream_t s);
+
 // Backward.
 struct BwdParams {
   const void* out;

@@ -193,6 +193,82 @@ int ffpa_bwd_varlen(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_t
                     const ffpa_tensor_t* dk, const ffpa_tensor_t* dv, ffpa_stream_t stream);
 
 /*
+ * A paged cache (the pages have no counterpart): K and V live in pages of
+ * `page` rows, k_cache and v_cache [pages, Hkv, page, D] with free strides
+ * (token-major pages [pages, page, Hkv, D] are a view), page 16, 32, 64 or a
+ * multiple of 128.  block_table, device int32 [B, max_pages], contiguous, gives
+ * the page that holds tokens k page .. (k + 1) page - 1 of request b.
+ *
+ * Lengths, tables and slots are read on the device: a captured call follows
+ * their new values at every replay.  What is out of range there is clamped or
+ * skipped, never used as an address, and ffpa_check_status then returns
+ * FFPA_ERR_INVALID_ARG.
+ *
+ * ffpa_fwd_tree: attention of drafted tokens over the cache.
+ *
+ *   q, out      [B, Hq, T, D], T <= 128 (1: plain decoding), Hkv divides Hq
+ *   max_pages   columns of block_table; max_pages * page <= 2^30
+ *   seq_lens    device int32 [B]: tokens of the request in the cache, its
+ *               drafted tokens included (they are the last ones)
+ *   draft_lens  nullable, device int32 [B]: drafted tokens m <= T of each
+ *               request (null: T each).  Rows i >= m are left as they are.
+ *   tree_mask   nullable, device bytes [mask_batch, T, T], contiguous,
+ *               mask_batch 1 or B: draft i sees draft j where byte (i, j) is not
+ *               0.  Null: j <= i.
+ *   lse         nullable, f32 [B, Hq, T, 1], contiguous
+ *
+ * Draft i sees every token before the drafts and the drafts its mask row
+ * marks.  A row that sees nothing gives 0 and lse -inf.  A request with
+ * seq_lens 0 (a padded batch's empty entry) has no rows and reads no page.
+ * Nothing behind a request's length is read, so unused rows of its last page
+ * may hold anything; the values of drafts that a mask hides must be finite.
+ * A missing page (number out of range) counts as zeros.
+ * Two launches; fp32 partials of at most 2 rows_n D floats per SM (rows_n 16,
+ * 32 or 64) in stream-ordered scratch.
+ */
+int ffpa_fwd_tree(const ffpa_tensor_t* q, const ffpa_tensor_t* k_cache, const ffpa_tensor_t* v_cache,
+                  const int32_t* block_table, int max_pages, const int32_t* seq_lens, const int32_t* draft_lens,
+                  const uint8_t* tree_mask, int mask_batch, float scale, const ffpa_tensor_t* out,
+                  const ffpa_tensor_t* lse, ffpa_stream_t stream);
+
+/*
+ * ffpa_cache_plan: pages, starts and slots of a step from request lengths.
+ * Request b holds lens[b] tokens and gets new_lens[b] more; its new pages are
+ * taken from free_pages, an array of n_free page numbers, from *free_head on,
+ * requests in order.
+ *
+ *   lens, new_lens   device int32 [n_reqs], not negative
+ *   page_size        any size >= 1
+ *   block_table      device int32 [n_reqs, max_pages]: the new pages' entries
+ *                    are written, the others are left
+ *   free_pages       device int32 [n_free]; free_head device int32 [1]
+ *   cu_new           device int32 [n_reqs + 1], written: first new token of
+ *                    each request in the packed batch (as ffpa_fwd_varlen takes it)
+ *   slots            device int64 [max_new], written: page * page_size + row of
+ *                    every packed new token, -1 behind the last one
+ *   lens_out         device int32 [n_reqs], written: lens + new_lens; may be lens
+ *   free_head_out    device int32 [1], written: first page still free; may be free_head
+ *
+ * Errors seen on the device (ffpa_check_status): a negative length (that
+ * request gets no tokens), no page left or no column left in the table (the
+ * entry is -1 or unwritten and the slot -1), more new tokens than max_new.
+ */
+int ffpa_cache_plan(const int32_t* lens, const int32_t* new_lens, int n_reqs, int page_size, int32_t* block_table,
+                    int max_pages, const int32_t* free_pages, int n_free, const int32_t* free_head, int32_t* cu_new,
+                    int64_t* slots, int64_t max_new, int32_t* lens_out, int32_t* free_head_out,
+                    ffpa_stream_t stream);
+
+/*
+ * ffpa_cache_append: writes the rows of k and v [1, Hkv, T, D] to their slots:
+ * row t goes to row slots[t] % page of page slots[t] / page.  slots is device
+ * int64 [T], contiguous; a negative slot skips its row, one past the last page
+ * is skipped and reported.  Slots that occur twice keep either row, possibly
+ * mixed in pieces of 8 elements.
+ */
+int ffpa_cache_append(const ffpa_tensor_t* k, const ffpa_tensor_t* v, const ffpa_tensor_t* k_cache,
+                      const ffpa_tensor_t* v_cache, const int64_t* slots, ffpa_stream_t stream);
+
+/*
  * ffpa_fwd_decode_noalloc: the decode forward (Nq <= 16) without allocating.
  * The pages have no counterpart; it exists for callers that cannot allocate
  * device memory during the call: code running under another framework's

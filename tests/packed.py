@@ -113,3 +113,56 @@ def check_varlen_bwd(q, k, v, lens, out, lse, dout, grads, causal, scale, first=
                     acc += x
             inside(dk[0, g, rows], sums[0], u * sums[0].abs() + sums[2], f"dK[seq {s}, head {g}]")
             inside(dv[0, g, rows], sums[1], u * sums[1].abs() + sums[3], f"dV[seq {s}, head {g}]")
+
+
+def paged(gen, host, lens, Hkv, page, D, dtype, spare=3, token_major=False, fill=None):
+    """Caches with the requests' tokens in shuffled pages, everything else `fill` (None: noise); the table and the
+    requests' dense K and V."""
+    counts = [(n + page - 1) // page for n in lens]
+    pages = sum(counts) + spare
+    shape = (pages, page, Hkv, D) if token_major else (pages, Hkv, page, D)
+    caches, dense = [], []
+    order = torch.randperm(pages, generator=host).tolist()
+    table = torch.full((len(lens), max(max(counts), 1)), -1, dtype=torch.int32)
+    used = 0
+    for b, c in enumerate(counts):
+        table[b, :c] = torch.tensor(order[used:used + c], dtype=torch.int32)
+        used += c
+    for _ in range(2):
+        c = torch.randn(shape, generator=gen, device="cuda").to(dtype) if fill is None else \
+            torch.full(shape, fill, dtype=dtype, device="cuda")
+        c = c.transpose(1, 2) if token_major else c
+        rows = []
+        for b, n in enumerate(lens):
+            x = torch.randn(n, Hkv, D, generator=gen, device="cuda").to(dtype)
+            for k in range(counts[b]):
+                part = x[k * page:(k + 1) * page]
+                c[int(table[b, k]), :, :part.shape[0]] = part.transpose(0, 1)
+            rows.append(x)
+        caches.append(c)
+        dense.append(rows)
+    return caches[0], caches[1], table.cuda(), dense[0], dense[1]
+
+
+def check_tree(q, dense_k, dense_v, lens, drafts, mask, out, lse, scale, untouched=None):
+    u = HALF_STEP[q.dtype]
+    B, Hq, T, D = q.shape
+    for b in range(B):
+        n, m = lens[b], drafts[b]
+        if untouched is not None:
+            assert bool((out[b, :, m:] == untouched).all()) and bool((lse[b, :, m:] == untouched).all()), f"rows past {m} of request {b}"
+        if m == 0:
+            continue
+        sees = torch.ones(m, n, dtype=torch.bool, device="cuda")
+        own = torch.ones(m, m, dtype=torch.bool, device="cuda").tril() if mask is None else \
+            mask[b if mask.shape[0] > 1 else 0, :m, :m]
+        sees[:, n - m:] = own
+        group = Hq // dense_k[b].shape[1]
+        for h in range(Hq):
+            o, l, pv = dense_fwd(q[b, h, :m], dense_k[b][:, h // group], dense_v[b][:, h // group], sees, scale)
+            inside(out[b, h, :m], o, u * o.abs() + (u + FP32) * pv, f"O[request {b}, head {h}]")
+            got = lse[b, h, :m].double()
+            gone = torch.isinf(l)
+            assert torch.equal(torch.isinf(got) & (got < 0), gone), f"lse[request {b}, head {h}]"
+            if not bool(gone.all()):
+                assert float((got - l)[~gone].abs().max()) <= LSE_ATOL, f"lse[request {b}, head {h}]"

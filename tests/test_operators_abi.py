@@ -80,3 +80,66 @@ def test_binding_checks_integer_tensors():
     for bad in (torch.zeros(4, dtype=torch.int64), torch.zeros(2, 2, dtype=torch.int32), torch.zeros(8, dtype=torch.int32)[::2]):
         with pytest.raises(ValueError, match="cu_seqlens"):
             _lib._ints(bad, "cu_seqlens", 1)
+
+
+# ------------------------------------------------------------------ paged cache
+
+def tree(B=2, Hq=4, Hkv=2, T=3, D=512, page=16, pages=9):
+    return {"q": t4([B, Hq, T, D]), "kc": t4([pages, Hkv, page, D]), "vc": t4([pages, Hkv, page, D]), "table": ADDR,
+            "max_pages": 4, "lens": ADDR, "drafts": ADDR, "mask": ADDR, "mask_batch": B, "scale": 0.05,
+            "out": t4([B, Hq, T, D]), "lse": t4([B, Hq, T, 1], dtype=_lib.FFPA_F32)}
+
+
+def fwd_tree(lib, a):
+    return lib.ffpa_fwd_tree(r(a["q"]), r(a["kc"]), r(a["vc"]), a["table"], a["max_pages"], a["lens"], a["drafts"],
+                             a["mask"], a["mask_batch"], a["scale"], r(a["out"]), r(a["lse"]), None)
+
+
+@pytest.mark.parametrize("name,value,expect", [
+    ("table", None, INVALID), ("lens", None, INVALID), ("lens", ADDR + 2, ALIGN), ("drafts", ADDR + 1, ALIGN),
+    ("max_pages", 0, INVALID), ("max_pages", 1 << 27, UNSUPPORTED), ("mask_batch", 3, INVALID), ("mask_batch", 0, INVALID),
+    ("scale", -1.0, INVALID), ("q", t4([2, 4, 129, 512]), UNSUPPORTED), ("q", t4([2, 5, 3, 512]), INVALID),
+    ("q", t4([2, 4, 3, 512], dtype=_lib.FFPA_F32), UNSUPPORTED), ("kc", t4([9, 2, 24, 512]), UNSUPPORTED),
+    ("kc", t4([9, 2, 8, 512]), UNSUPPORTED), ("kc", t4([9, 2, 16, 448]), INVALID), ("kc", None, INVALID),
+    ("vc", t4([8, 2, 16, 512]), INVALID), ("vc", t4([9, 2, 16, 512], dtype=_lib.FFPA_F16), INVALID),
+    ("out", t4([2, 4, 4, 512]), INVALID), ("lse", t4([2, 4, 4, 1], dtype=_lib.FFPA_F32), INVALID),
+    ("kc", t4([9, 2, 16, 512], addr=ADDR + 8), ALIGN),
+])
+def test_tree_rejects(lib, name, value, expect):
+    a = tree()
+    a[name] = value
+    assert fwd_tree(lib, a) == expect
+
+
+def plan(lib, **over):
+    a = dict(lens=ADDR, new=ADDR, n=3, page=16, table=ADDR, per=4, free=ADDR, n_free=5, head=ADDR, cu=ADDR, slots=ADDR,
+             max_new=7, lens_out=ADDR, head_out=ADDR)
+    a.update(over)
+    return lib.ffpa_cache_plan(a["lens"], a["new"], a["n"], a["page"], a["table"], a["per"], a["free"], a["n_free"],
+                               a["head"], a["cu"], a["slots"], a["max_new"], a["lens_out"], a["head_out"], None)
+
+
+@pytest.mark.parametrize("over,expect", [
+    (dict(lens=None), INVALID), (dict(new=None), INVALID), (dict(table=None), INVALID), (dict(free=None), INVALID),
+    (dict(head=None), INVALID), (dict(cu=None), INVALID), (dict(slots=None), INVALID), (dict(lens_out=None), INVALID),
+    (dict(head_out=None), INVALID), (dict(n=0), INVALID), (dict(page=0), INVALID), (dict(per=0), INVALID),
+    (dict(n_free=-1), INVALID), (dict(max_new=-1), INVALID), (dict(max_new=(1 << 30) + 1), UNSUPPORTED),
+    (dict(slots=ADDR + 4), ALIGN), (dict(lens=ADDR + 2), ALIGN),
+])
+def test_plan_rejects(lib, over, expect):
+    assert plan(lib, **over) == expect
+
+
+@pytest.mark.parametrize("name,value,expect", [
+    ("k", None, INVALID), ("slots", None, INVALID), ("slots", ADDR + 4, ALIGN), ("v", t4([1, 2, 6, 512]), INVALID),
+    ("k", t4([2, 2, 5, 512]), INVALID), ("kc", t4([9, 3, 16, 512]), INVALID), ("vc", t4([9, 2, 24, 512]), INVALID),
+    ("k", t4([1, 2, 5, 96]), UNSUPPORTED), ("k", t4([1, 2, 5, 512], dtype=_lib.FFPA_F32), UNSUPPORTED),
+    ("kc", t4([9, 2, 16, 512], dtype=_lib.FFPA_F16), INVALID), ("v", t4([1, 2, 5, 512], addr=ADDR + 2), ALIGN),
+])
+def test_append_rejects(lib, name, value, expect):
+    a = {"k": t4([1, 2, 5, 512]), "v": t4([1, 2, 5, 512]), "kc": t4([9, 2, 16, 512]), "vc": t4([9, 2, 16, 512]),
+         "slots": ADDR}
+    a[name] = value
+    if name == "k" and value is not None and value.shape[3] == 96:
+        a["v"] = value
+    assert lib.ffpa_cache_append(r(a["k"]), r(a["v"]), r(a["kc"]), r(a["vc"]), a["slots"], None) == expect
