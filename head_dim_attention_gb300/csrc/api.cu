@@ -710,11 +710,11 @@ int fwd_tree_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* kc, const ffpa_te
   p.max_pages = max_pages;
   p.scale_log2 = scale * kLog2e;
   const int64_t rows = static_cast<int64_t>(p.group) * p.T;
-  p.rows_n = tree_rows_n(static_cast<int>(std::min<int64_t>(rows, 1 << 20)), p.D);
-  // as many blocks as there can be key tiles to share out, one per SM at most
+  const int most = tree_shape(&p, rows) * sms;
+  // as many blocks as there can be key tiles to share out
   const int64_t units = c.B * c.Hkv * ((rows + p.rows_n - 1) / p.rows_n);
   const int64_t tiles = (static_cast<int64_t>(max_pages) * p.page + kTileRows - 1) / kTileRows;
-  p.blocks = static_cast<int>(units >= sms || tiles >= sms ? sms : std::min<int64_t>(units * tiles, sms));
+  p.blocks = static_cast<int>(units >= most || tiles >= most ? most : std::min<int64_t>(units * tiles, most));
   p.status = status;
   CUtensorMap mk, mv;
   const int box = std::min(p.page, kTileRows);

@@ -9,9 +9,9 @@
 //
 // What bounds it: reading K and V once, 4 D bytes per key and kv head.  A tile
 // of 128 query rows would be mostly padding, so the operands are swapped: keys
-// and head-dimension columns are the MMA's M, the rows its N (16, 32 or 64):
+// and head-dimension columns are the MMA's M, the rows its N (16, 32, 64 or 96):
 //   S^T [128 keys, N]  = K_tile (K-major A) . Q^T (K-major B)
-//   O^T [128 columns, N] += V_tile^T (MN-major A) . P^T (MN-major B)
+//   O^T [128 columns, N] += V_tile^T (MN-major A) . P^T (K-major B)
 // O^T of all D columns stays in TMEM (ceil(D / 128) N columns of 512), the S^T
 // buffers above it, and the tensor work follows the rows there are.
 //
@@ -35,8 +35,8 @@
 //
 // Warps: 0 and 2 TMA producers (alternate ring slots; the lanes of a warp issue
 // a slot's boxes), 1 TMEM owner and MMA issuer, from 4 on softmax, correction
-// and epilogue: one warpgroup for N <= 32, two for N = 64 (32 rows each; thread
-// = key of S^T, then column of O^T).  Every wait is bounded.
+// and epilogue: a warpgroup per 32 rows (thread = key of S^T, then column of
+// O^T).  Every wait is bounded.
 #include <algorithm>
 #include <type_traits>
 
@@ -46,8 +46,8 @@
 namespace ffpa {
 namespace {
 
-constexpr int kSlotBytes = 2 * kChunkBytes;  // two 64-column chunks of 128 keys
-constexpr int kPBytes = kTileRows * 128;     // 128 keys x 64 rows of 16 bits
+// P of a key tile: two halves of 64 keys, each N rows of 128 bytes
+constexpr int p_bytes(int N) { return 2 * N * 128; }
 constexpr int kMaxSlots = 6;
 constexpr int kMaxSmem = 232448;
 constexpr float kRescaleLog2 = 8.0f;  // rescale O only when a row's max grows by > 2^8
@@ -91,6 +91,7 @@ __device__ __forceinline__ int64_t request_work(const TreeParams& p, const Reque
 struct WorkSum {
   int64_t before_run, run, total;
   int first, last;  // requests of this thread's run
+  Request r;        // the first of them
 };
 template <int N>
 __device__ __forceinline__ WorkSum sum_work(const TreeParams& p, int64_t* sums, int threads) {
@@ -100,7 +101,12 @@ __device__ __forceinline__ WorkSum sum_work(const TreeParams& p, int64_t* sums, 
   w.first = min(p.B, tid * per);
   w.last = min(p.B, w.first + per);
   w.run = 0;
-  for (int b = w.first; b < w.last; ++b) w.run += request_work<N>(p, request(p, b));
+  w.r = {0, 0};
+  if (w.first < w.last) {
+    w.r = request(p, w.first);
+    w.run = request_work<N>(p, w.r);
+    for (int b = w.first + 1; b < w.last; ++b) w.run += request_work<N>(p, request(p, b));
+  }
   int64_t incl = w.run;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -132,8 +138,7 @@ struct Walk {
   int hk, row0;        // kv head, first row of the row tile
   int end;             // one past the segment's last key tile
 
-  __device__ __forceinline__ void load(const TreeParams& p) {
-    r = request(p, b);
+  __device__ __forceinline__ void shape(const TreeParams& p) {
     rt = row_tiles<N>(p, r);
     tiles = key_tiles(r);
   }
@@ -142,13 +147,15 @@ struct Walk {
     row0 = (sub % rt) * N;
     end = static_cast<int>(min(static_cast<int64_t>(tiles), tile + left));
   }
-  // `offset`: the block's first tile within request b0's work
-  __device__ __forceinline__ void begin(const TreeParams& p, int b0, int64_t offset, int64_t count) {
+  // `offset`: the block's first tile within the request's work
+  __device__ __forceinline__ void begin(const TreeParams& p, int request_index, const Request& rq, int64_t offset,
+                                        int64_t count) {
     left = count;
-    b = b0;
-    load(p);
+    b = request_index;
+    r = rq;
+    shape(p);
     sub = static_cast<int>(offset / tiles);
-    tile = static_cast<int>(offset % tiles);
+    tile = static_cast<int>(offset - static_cast<int64_t>(sub) * tiles);
     place();
   }
   // to the next segment; false when the block's tiles are used up
@@ -161,7 +168,8 @@ struct Walk {
       do {
         ++b;
         if (b >= p.B) return false;
-        load(p);
+        r = request(p, b);
+        shape(p);
       } while (tiles == 0 || rt == 0);
     }
     place();
@@ -178,11 +186,12 @@ __host__ __device__ constexpr Bars bar_layout() {
               2 * kMaxSlots + 6, 2 * kMaxSlots + 7, 2 * kMaxSlots + 8, 2 * kMaxSlots + 9};
 }
 
-constexpr int kMiscBytes = 256 /* barriers, TMEM base, start */ + 8 * 128 /* work sums */ + 128 * 8 /* vis */ +
-                           64 * 8 * 2 /* rows in out and lse */ + 12 * 32 * 4 * 2 /* statistics */;
+constexpr int kMiscBytes = 256 /* barriers, TMEM base, start */ + 128 /* work sums */ + 3 * 128 * 4 /* vis */ +
+                           96 * 8 * 2 /* rows in out and lse */ + 12 * 32 * 4 * 2 /* statistics */;
+static_assert(kMiscBytes % 128 == 0, "tile alignment");
 __host__ __device__ constexpr int q_bytes(int n_chunks, int N) { return n_chunks * N * 128; }
 __host__ __device__ constexpr int fixed_bytes(int n_chunks, int N) {
-  return q_bytes(n_chunks, N) + 2 * kPBytes + kMiscBytes + 1024;
+  return q_bytes(n_chunks, N) + 2 * p_bytes(N) + kMiscBytes + 1024;
 }
 
 template <bool BF16>
@@ -211,6 +220,9 @@ __device__ __forceinline__ void store1(void* base, int64_t at, float x) {
 }
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
+  asm volatile("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tst.shared.b16 [%0], h;\n\t}" ::"r"(addr), "r"(v) : "memory");
 }
 // All `threads` threads meet; true if every one of them passes true.
 __device__ __forceinline__ bool bar_and(uint32_t id, uint32_t threads, bool v) {
@@ -276,35 +288,43 @@ __device__ __forceinline__ float reduce_columns(float (&v)[C], int lane, Op op) 
 
 template <int N>
 constexpr int tree_threads() {
-  return N == 64 ? 384 : 256;
+  return 128 + 128 * ((N + 31) / 32);
+}
+// Blocks per SM the registers allow for: two for N <= 32 (launched as two where
+// the shared memory of a small D allows it, see launch_n).
+template <int N>
+constexpr int tree_residency() {
+  return N <= 32 ? 2 : 1;
 }
 
 template <int N, bool BF16>
-__global__ void __launch_bounds__(tree_threads<N>(), 1)
+__global__ void __launch_bounds__(tree_threads<N>(), tree_residency<N>())
     tree_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                 const __grid_constant__ TreeParams p) {
   typedef typename std::conditional<BF16, __nv_bfloat16, __half>::type T;
   constexpr int kThreads = tree_threads<N>();
   constexpr int kSoftWarps = kThreads / 32 - 4;
-  constexpr int C = N == 64 ? 32 : N;  // rows per softmax thread
+  constexpr int C = N < 32 ? N : 32;       // rows per softmax thread
+  constexpr int kSBuf = N == 96 ? 1 : 2;   // S^T buffers: TMEM has room for one next to a 96-row O^T
   constexpr Bars bl = bar_layout();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int NC = p.n_chunks, slots = p.slots;
-  const uint32_t ring = smem_u32(smem), p_hi = ring + slots * kSlotBytes, p_lo = p_hi + kPBytes;
-  const uint32_t q_sm = p_lo + kPBytes;
-  uint8_t* misc = smem + slots * kSlotBytes + 2 * kPBytes + q_bytes(NC, N);
+  const uint32_t slot_bytes = p.slot_bytes;
+  const uint32_t ring = smem_u32(smem), p_hi = ring + slots * slot_bytes, p_lo = p_hi + p_bytes(N);
+  const uint32_t q_sm = p_lo + p_bytes(N);
+  uint8_t* misc = smem + slots * slot_bytes + 2 * p_bytes(N) + q_bytes(NC, N);
   uint64_t* bars = reinterpret_cast<uint64_t*>(misc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + bl.count);
-  int64_t* start = reinterpret_cast<int64_t*>(misc + 232);  // [3]: request, offset in its work, tiles of this block
+  Walk<N>* start = reinterpret_cast<Walk<N>*>(misc + 176);  // the block's first segment (left == 0: none)
   int64_t* sums = reinterpret_cast<int64_t*>(misc + 256);
-  uint64_t* vis = reinterpret_cast<uint64_t*>(misc + 256 + 1024);      // [128] draft -> rows that see it
-  int64_t* row_off = reinterpret_cast<int64_t*>(vis + 128);            // [N] offset of the row in out, -1: padding
-  int64_t* row_lse = row_off + 64;                                     // [N] index of the row in lse
-  float* stat = reinterpret_cast<float*>(row_lse + 64);                // [warps][32] exchanged statistics
+  uint32_t* vis = reinterpret_cast<uint32_t*>(misc + 256 + 128);       // [3][128] draft -> rows that see it, 32 rows each
+  int64_t* row_off = reinterpret_cast<int64_t*>(vis + 3 * 128);        // [N] offset of the row in out, -1: padding
+  int64_t* row_lse = row_off + 96;                                     // [N] index of the row in lse
+  float* stat = reinterpret_cast<float*>(row_lse + 96);                // [warps][32] exchanged statistics
   float* bcast = stat + 12 * 32;                                       // [warps][32] per-row values of one warp
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
-  static_assert(bl.count * 8 + 8 <= 232, "barrier area");
+  static_assert(bl.count * 8 + 4 <= 176 && 176 + sizeof(Walk<N>) <= 256, "barrier area");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t* status = p.status;
@@ -314,7 +334,7 @@ __global__ void __launch_bounds__(tree_threads<N>(), 1)
       mbar_init(bar(bl.empty + i), 1);
     }
     mbar_init(bar(bl.q_full), kSoftWarps);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kSBuf; ++i) {
       mbar_init(bar(bl.s_full + i), 1);
       mbar_init(bar(bl.s_free + i), kSoftWarps);
     }
@@ -323,11 +343,15 @@ __global__ void __launch_bounds__(tree_threads<N>(), 1)
     mbar_init(bar(bl.o_free), kSoftWarps);
     mbar_init(bar(bl.drain), 1);
     fence_mbar_init();
-    start[2] = 0;
+    start->left = 0;
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_alloc(smem_u32(tmem_slot), p.tmem_cols);
     tmem_relinquish();
+  }
+  if (warp == 2 && lane == 0) {
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
   }
   tc_fence_before();
   {
@@ -339,35 +363,28 @@ __global__ void __launch_bounds__(tree_threads<N>(), 1)
         const int64_t w0 = block_start(w.total, blocks, c), w1 = block_start(w.total, blocks, c + 1);
         if (w0 >= w.before_run && w0 < w.before_run + w.run) {
           int64_t at = w.before_run;
-          for (int b = w.first; b < w.last; ++b) {
-            const int64_t x = request_work<N>(p, request(p, b));
-            if (w0 < at + x) {
-              start[0] = b;
-              start[1] = w0 - at;
-              start[2] = w1 - w0;
-              break;
-            }
-            at += x;
+          int b = w.first;
+          Request r = w.r;
+          while (w0 >= at + request_work<N>(p, r)) {
+            at += request_work<N>(p, r);
+            r = request(p, ++b);
           }
+          Walk<N> first;
+          first.begin(p, b, r, w0 - at, w1 - w0);
+          *start = first;
         }
       }
     }
   }
   __syncthreads();
-  if (tid == 0) {
-    // where this block starts, for the merge kernel
-    int4 at = make_int4(-1, 0, 0, 0);
-    if (start[2] > 0) {
-      Walk<N> w;
-      w.begin(p, static_cast<int>(start[0]), start[1], start[2]);
-      at = make_int4(w.b, w.sub, w.tile, 0);
-    }
-    p.starts[blockIdx.x] = at;
-  }
+  // where this block starts, for the merge kernel
+  if (tid == 0)
+    p.starts[blockIdx.x] = start->left > 0 ? make_int4(start->b, start->sub, start->tile, start->r.m) : make_int4(-1, 0, 0, 0);
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-  const bool any = start[2] > 0;
-  const uint32_t s_tm = 512 - 2 * N;  // the two S^T buffers above O^T
+  const bool any = start->left > 0;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge kernel's blocks may take free room
+  const uint32_t s_tm = p.tmem_cols - kSBuf * N;  // the S^T buffers above O^T
   const int kslots = (NC + 1) / 2;    // ring slots of one key tile of K, or of V
 
   if (any && (warp == 0 || warp == 2)) {
@@ -377,10 +394,6 @@ __global__ void __launch_bounds__(tree_threads<N>(), 1)
     // neither runs a round ahead of a slot's barrier).
     const int pi = warp >> 1;
     const int box = min(p.page, kTileRows), pieces = kTileRows / box;
-    if (lane == 0) {
-      tma_prefetch_desc(&map_k);
-      tma_prefetch_desc(&map_v);
-    }
     bool ok = true;
     uint32_t it = 0;
     // one key tile of K or V: lane l issues box l of each slot (piece l mod pieces, chunk l / pieces)
@@ -406,12 +419,11 @@ __global__ void __launch_bounds__(tree_threads<N>(), 1)
         if (lane == 0) mbar_expect_tx(bar(bl.full + s), cn * kChunkBytes);
         __syncwarp();
         if (ch < cn)
-          tma_load_4d(ring + s * kSlotBytes + ch * kChunkBytes + piece * box * 128, m, bar(bl.full + s),
+          tma_load_4d(ring + s * slot_bytes + ch * kChunkBytes + piece * box * 128, m, bar(bl.full + s),
                       (2 * s2 + ch) * kChunk, row, w.hk, page);
       }
     };
-    Walk<N> w;
-    w.begin(p, static_cast<int>(start[0]), start[1], start[2]);
+    Walk<N> w = *start;
     do {
       load_tile(&map_k, w, w.tile);
       for (int t = w.tile; t < w.end && ok; ++t) {
@@ -429,19 +441,19 @@ __global__ void __launch_bounds__(tree_threads<N>(), 1)
   } else if (any && warp == 1 && lane == 0) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t idesc_s = idesc_f16(BF16, 128, N, false, false);
-    constexpr uint32_t idesc_o = idesc_f16(BF16, 128, N, true, true);
+    constexpr uint32_t idesc_o = idesc_f16(BF16, 128, N, true, false);
     const uint64_t dk = sdesc_sw128(ring, 16, 1024), dv = sdesc_sw128(ring, kChunkBytes, 1024);
     const uint64_t dq = sdesc_sw128(q_sm, 16, 1024);
     const uint64_t dhi = sdesc_sw128(p_hi, 16, 1024), dlo = sdesc_sw128(p_lo, 16, 1024);
     bool ok = true;
     uint32_t it = 0, tc = 0, unit = 0;  // ring loads, S^T tiles and units so far
     auto scores = [&]() {
-      if (tc >= 2) {
-        ok = mbar_wait<false>(bar(bl.s_free + (tc & 1)), ((tc - 2) >> 1) & 1, status);
+      if (tc >= kSBuf) {
+        ok = mbar_wait<false>(bar(bl.s_free + tc % kSBuf), ((tc - kSBuf) / kSBuf) & 1, status);
         if (!ok) return;
         tc_fence_after();
       }
-      const uint32_t d = tbase + s_tm + (tc & 1) * N;
+      const uint32_t d = tbase + s_tm + (tc % kSBuf) * N;
       for (int s2 = 0; s2 < kslots; ++s2, ++it) {
         const uint32_t s = it % slots;
         ok = mbar_wait<false>(bar(bl.full + s), (it / slots) & 1, status);
@@ -449,7 +461,7 @@ __global__ void __launch_bounds__(tree_threads<N>(), 1)
         tc_fence_after();
         const int cn = min(2, NC - 2 * s2);
         for (int i = 0; i < cn; ++i) {
-          const uint64_t a = sdesc_advance(dk, s * kSlotBytes + i * kChunkBytes);
+          const uint64_t a = sdesc_advance(dk, s * slot_bytes + i * kChunkBytes);
           const uint64_t b = sdesc_advance(dq, (2 * s2 + i) * N * 128);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
@@ -457,11 +469,10 @@ __global__ void __launch_bounds__(tree_threads<N>(), 1)
         }
         umma_commit(bar(bl.empty + s));
       }
-      umma_commit(bar(bl.s_full + (tc & 1)));
+      umma_commit(bar(bl.s_full + tc % kSBuf));
       ++tc;
     };
-    Walk<N> w;
-    w.begin(p, static_cast<int>(start[0]), start[1], start[2]);
+    Walk<N> w = *start;
     uint32_t pv = 0;  // P V products so far
     do {
       ok = mbar_wait<false>(bar(bl.q_full), unit & 1, status);
@@ -485,14 +496,16 @@ __global__ void __launch_bounds__(tree_threads<N>(), 1)
           tc_fence_after();
           // columns 128 s2 .. of O^T; at an odd chunk count the last slot's second
           // half is stale shared memory: it reaches only O^T rows past D
-          const uint64_t a = sdesc_advance(dv, s * kSlotBytes);
+          const uint64_t a = sdesc_advance(dv, s * slot_bytes);
           const uint32_t d = tbase + s2 * N;
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
-            umma_ss(d, sdesc_advance(a, ks * 2048), sdesc_advance(dhi, ks * 2048), idesc_o, t > w.tile || ks > 0);
+            umma_ss(d, sdesc_advance(a, ks * 2048), sdesc_advance(dhi, (ks >> 2) * (N * 128) + (ks & 3) * 32), idesc_o,
+                    t > w.tile || ks > 0);
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
-            umma_ss(d, sdesc_advance(a, ks * 2048), sdesc_advance(dlo, ks * 2048), idesc_o, 1u);
+            umma_ss(d, sdesc_advance(a, ks * 2048), sdesc_advance(dlo, (ks >> 2) * (N * 128) + (ks & 3) * 32), idesc_o,
+                    1u);
           umma_commit(bar(bl.empty + s));
         }
         if (!ok) break;
@@ -518,12 +531,11 @@ __global__ void __launch_bounds__(tree_threads<N>(), 1)
     constexpr float kLn2 = 0.6931471805599453f;
     bool ok = true;
     uint32_t tc = 0;
-    Walk<N> w;
-    w.begin(p, static_cast<int>(start[0]), start[1], start[2]);
+    Walk<N> w = *start;
     do {
       const int m = w.r.m, n = w.r.n, prefix = n - m, rows = p.group * m;
       // ---- the unit: row offsets, draft visibility, Q
-      if (!bar_and(3, kAll, ok)) break;  // the epilogue before has read the tables
+      if (!bar_and(4, kAll, ok)) break;  // the epilogue before has read the tables
       if (st < N) {
         const int rr = w.row0 + st;
         int64_t off = -1;
@@ -537,61 +549,75 @@ __global__ void __launch_bounds__(tree_threads<N>(), 1)
         row_lse[st] = li;
       }
       if (w.end * kTileRows > prefix) {  // this segment has drafts among its keys
-        for (int j = st; j < m; j += kAll) {
-          uint64_t bits = 0;
-          for (int x = 0; x < N; ++x) {
-            const int rr = w.row0 + x;
+        // item (draft j, 32 rows g): a bit for each row that sees the draft
+        for (int it = st; it < ((N + 31) / 32) * m; it += kAll) {
+          const int j = it % m, g = it / m;
+          uint32_t bits = 0;
+          for (int x = 0; x < C; ++x) {
+            const int rr = w.row0 + g * 32 + x;
             if (rr >= rows) break;
             const int i = rr % m;
             const bool see = p.mask ? __ldg(p.mask + w.b * p.mask_sb + static_cast<int64_t>(i) * p.T + j) != 0 : j <= i;
-            if (see) bits |= 1ull << x;
+            if (see) bits |= 1u << x;
           }
-          vis[j] = bits;
+          vis[g * 128 + j] = bits;
         }
       }
-      // Q rows of the tile, K-major with the 128-byte swizzle; padding rows zero
-      const int vecs = N * NC * 8;  // 16-byte pieces: piece v is row v / (8 NC), granule v % (8 NC)
-      for (int v0 = st; v0 < vecs; v0 += 8 * kAll) {
-        uint4 x[8];
+      // Q rows of the tile, K-major with the 128-byte swizzle; padding rows zero.
+      // A warp takes rows sw, sw + kSoftWarps, ..: four at a time, two 16-byte
+      // granules of each per lane, all in flight together.
+      for (int r0 = sw; r0 < N; r0 += 4 * kSoftWarps) {
+        const uint4* src[4];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int v = v0 + u * kAll, rr = w.row0 + v / (8 * NC), gq = v % (8 * NC);
-          x[u] = make_uint4(0u, 0u, 0u, 0u);
-          if (v < vecs && rr < rows)
-            x[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + w.b * p.q_sb +
-                                                        (w.hk * p.group + rr / m) * p.q_sh + (rr % m) * p.q_sn) +
-                         gq);
+        for (int u = 0; u < 4; ++u) {
+          const int rr = w.row0 + r0 + u * kSoftWarps;
+          src[u] = nullptr;
+          if (rr < rows)
+            src[u] = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + w.b * p.q_sb +
+                                                    (w.hk * p.group + rr / m) * p.q_sh + (rr % m) * p.q_sn);
         }
+        for (int g0 = lane; g0 < 8 * NC; g0 += 64) {
+          uint4 x[4][2];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int v = v0 + u * kAll, r = v / (8 * NC), gq = v % (8 * NC);
-          if (v < vecs)
-            st_shared_v4(q_sm + (gq >> 3) * (N * 128) + r * 128 + (((gq & 7) ^ (r & 7)) << 4), x[u].x, x[u].y, x[u].z,
-                         x[u].w);
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              x[u][e] = make_uint4(0u, 0u, 0u, 0u);
+              if (src[u] && g0 + 32 * e < 8 * NC) x[u][e] = __ldg(src[u] + g0 + 32 * e);
+            }
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int r = r0 + u * kSoftWarps, gq = g0 + 32 * e;
+              if (r < N && gq < 8 * NC)
+                st_shared_v4(q_sm + (gq >> 3) * (N * 128) + r * 128 + (((gq & 7) ^ (r & 7)) << 4), x[u][e].x,
+                             x[u][e].y, x[u][e].z, x[u][e].w);
+            }
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(bl.q_full));
-      if (!bar_and(3, kAll, ok)) break;  // tables written
+      if (!bar_and(4, kAll, ok)) break;  // tables written
 
       float l[C];  // this key's share of the rows' sums
 #pragma unroll
       for (int x = 0; x < C; ++x) l[x] = 0.f;
       float m_used = -INFINITY;  // lane x mod C: reference maximum of row x (log2 domain), the same in all warps
       for (int tile = w.tile; tile < w.end; ++tile, ++tc) {
-        if (ok) ok = mbar_wait<false>(bar(bl.s_full + (tc & 1)), (tc >> 1) & 1, status);
+        if (ok) ok = mbar_wait<false>(bar(bl.s_full + tc % kSBuf), (tc / kSBuf) & 1, status);
         ok = __all_sync(0xffffffffu, ok);
         float s[C];
         if (ok) {
           tc_fence_after();
           uint32_t v[C];
-          tmem_load<C>(tbase + lane_off + s_tm + (tc & 1) * N + wg * C, v);
+          tmem_load<C>(tbase + lane_off + s_tm + (tc % kSBuf) * N + wg * C, v);
 #pragma unroll
           for (int x = 0; x < C; ++x) s[x] = __uint_as_float(v[x]);
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(bl.s_free + (tc & 1)));
+          if (lane == 0) mbar_arrive(bar(bl.s_free + tc % kSBuf));
         } else {
 #pragma unroll
           for (int x = 0; x < C; ++x) s[x] = 0.f;
@@ -605,7 +631,7 @@ __global__ void __launch_bounds__(tree_threads<N>(), 1)
           if (r < shift)
             see = 0u;
           else if (pos >= prefix)
-            see = static_cast<uint32_t>(vis[pos - prefix] >> (wg * C));
+            see = vis[wg * 128 + pos - prefix];
 #pragma unroll
           for (int x = 0; x < C; ++x)
             if (!((see >> x) & 1u)) s[x] = -INFINITY;
@@ -632,27 +658,10 @@ __global__ void __launch_bounds__(tree_threads<N>(), 1)
           my_bcast[lane] = m_used == -INFINITY ? 0.f : m_used;
           __syncwarp();
         }
-        // P (and its rounding residual) of this key
-        uint32_t hi[C / 2], lo[C / 2];
         const bool rescale = __any_sync(0xffffffffu, alpha != 1.f);  // the same in the four warps
         if (rescale) {
 #pragma unroll
           for (int x = 0; x < C; ++x) l[x] *= __shfl_sync(0xffffffffu, alpha, x);
-        }
-#pragma unroll
-        for (int x = 0; x < C; x += 4) {
-          const float4 ref = *reinterpret_cast<const float4*>(my_bcast + x);
-          const float p0 = ex2(fmaf(s[x], p.scale_log2, -ref.x)), p1 = ex2(fmaf(s[x + 1], p.scale_log2, -ref.y));
-          const float p2 = ex2(fmaf(s[x + 2], p.scale_log2, -ref.z)), p3 = ex2(fmaf(s[x + 3], p.scale_log2, -ref.w));
-          l[x] += p0;
-          l[x + 1] += p1;
-          l[x + 2] += p2;
-          l[x + 3] += p3;
-          hi[x / 2] = pack2<BF16>(p0, p1);
-          hi[x / 2 + 1] = pack2<BF16>(p2, p3);
-          const float2 a = unpack2<BF16>(hi[x / 2]), b = unpack2<BF16>(hi[x / 2 + 1]);
-          lo[x / 2] = pack2<BF16>(p0 - a.x, p1 - a.y);
-          lo[x / 2 + 1] = pack2<BF16>(p2 - b.x, p3 - b.y);
         }
         if (tc > 0) {  // the product before has read P and written O^T
           if (ok) ok = mbar_wait<false>(bar(bl.pv_done), (tc - 1) & 1, status);
@@ -671,13 +680,27 @@ __global__ void __launch_bounds__(tree_threads<N>(), 1)
           }
           tmem_st_wait();
         }
-        {
-          const uint32_t row = static_cast<uint32_t>(t) * 128u;
+        // P and its rounding residual of this key: row wg C + x of the key's half,
+        // granule (t mod 64) / 8 under the 128-byte swizzle
+        const uint32_t key_at = (t >> 6) * (N * 128) + wg * C * 128 + (t & 7) * 2, gran = (t & 63) >> 3;
 #pragma unroll
-          for (int g = 0; g < C / 8; ++g) {
-            const uint32_t at = row + (static_cast<uint32_t>((wg * (C / 8) + g) ^ (t & 7)) << 4);
-            st_shared_v4(p_hi + at, hi[4 * g], hi[4 * g + 1], hi[4 * g + 2], hi[4 * g + 3]);
-            st_shared_v4(p_lo + at, lo[4 * g], lo[4 * g + 1], lo[4 * g + 2], lo[4 * g + 3]);
+        for (int x = 0; x < C; x += 4) {
+          const float4 ref = *reinterpret_cast<const float4*>(my_bcast + x);
+          const float e[4] = {ex2(fmaf(s[x], p.scale_log2, -ref.x)), ex2(fmaf(s[x + 1], p.scale_log2, -ref.y)),
+                              ex2(fmaf(s[x + 2], p.scale_log2, -ref.z)), ex2(fmaf(s[x + 3], p.scale_log2, -ref.w))};
+#pragma unroll
+          for (int u = 0; u < 4; u += 2) {
+            l[x + u] += e[u];
+            l[x + u + 1] += e[u + 1];
+            const uint32_t hi = pack2<BF16>(e[u], e[u + 1]);
+            const float2 r = unpack2<BF16>(hi);
+            const uint32_t lo = pack2<BF16>(e[u] - r.x, e[u + 1] - r.y);
+            const uint32_t at0 = key_at + (x + u) * 128 + ((gran ^ ((x + u) & 7)) << 4);
+            const uint32_t at1 = key_at + (x + u + 1) * 128 + ((gran ^ ((x + u + 1) & 7)) << 4);
+            st_shared_u16(p_hi + at0, hi);
+            st_shared_u16(p_hi + at1, hi >> 16);
+            st_shared_u16(p_lo + at0, lo);
+            st_shared_u16(p_lo + at1, lo >> 16);
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -711,6 +734,8 @@ __global__ void __launch_bounds__(tree_threads<N>(), 1)
           p.lse[row_lse[wg * C + lane]] = sum > 0.f ? (m_used + __log2f(sum)) * kLn2 : -INFINITY;
       } else {
         const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (w.tile > 0 ? 0 : 1);
+        const int mine = rows - w.row0 - wg * C;  // of this warpgroup's rows, those that are not padding
+        float* part = p.part_o + (slot * N + wg * C) * p.D;
         for (int blk = 0; blk < kslots; ++blk) {
           uint32_t v[C];
           tmem_load<C>(tbase + lane_off + blk * N + wg * C, v);
@@ -718,7 +743,7 @@ __global__ void __launch_bounds__(tree_threads<N>(), 1)
           if (d < p.D) {
 #pragma unroll
             for (int x = 0; x < C; ++x)
-              if (row_off[wg * C + x] >= 0) p.part_o[(slot * N + wg * C + x) * p.D + d] = __uint_as_float(v[x]);
+              if (x < mine) part[x * p.D + d] = __uint_as_float(v[x]);
           }
         }
         if ((warp & 3) == 0 && lane < C) {
@@ -737,79 +762,104 @@ __global__ void __launch_bounds__(tree_threads<N>(), 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tbase, 512);
+    tmem_dealloc(tbase, p.tmem_cols);
   }
 }
 
-// Joins the partials of the units that cross blocks.  Block (c, x) looks at the
+// Joins the partials of the units that cross blocks.  Block (c, y) looks at the
 // place where attention block c starts: if that is inside a unit, and the
-// first such place in it, it merges row x of the unit.  The unit's first piece
-// is slot 1 of block c - 1, the others slot 0 of the blocks from c on.
+// first such place in it, its warps merge rows 4 y .. of the unit, one each.  The
+// unit's first piece is slot 1 of block c - 1, the others slot 0 of the blocks
+// from c on.
 //   O = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c
-template <int N, bool BF16>
-__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p) {
+// Latency bounds it (three dependent reads and, per 32 pieces, one round of
+// loads), so many small blocks: a warp per row, Q = ceil(D / 128) to a power of
+// two float4 of it per lane.
+template <int N, bool BF16, int Q>
+__global__ void __launch_bounds__(kMergeThreads, Q == 8 ? 5 : 8) tree_merge_kernel(const __grid_constant__ TreeParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x + 1, x = blockIdx.y;
-  const int4 at = p.starts[c], prev = p.starts[c - 1];
-  if (at.x < 0 || at.z == 0) return;                                  // idle, or at a unit's start
-  if (prev.x == at.x && prev.y == at.y && prev.z > 0) return;         // not the first
-  const int b = at.x, sub = at.y;
-  const Request r = request(p, b);
-  const int rt = row_tiles<N>(p, r);
+  const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int x = blockIdx.y * (kMergeThreads / 32) + warp;
+  const int4 prev = p.starts[c - 1], at = p.starts[c];
+  // the starts that follow, 32 at a time: how many more are inside the unit
+  int4 next = make_int4(-1, 0, 0, 0);
+  if (c + 1 + lane < p.blocks) next = p.starts[c + 1 + lane];
+  if (at.x < 0 || at.z == 0) return;                           // idle, or at a unit's start
+  if (prev.x == at.x && prev.y == at.y && prev.z > 0) return;  // not the first
+  const int b = at.x, sub = at.y, m = at.w;
+  const int rt = (p.group * m + N - 1) / N;
   const int rr = (sub % rt) * N + x;
-  if (rr >= p.group * r.m) return;
-  const int h = (sub / rt) * p.group + rr / r.m, i = rr % r.m;
+  if (x >= N || rr >= p.group * m) return;
   int pieces = 2;
-  while (c + pieces - 1 < p.blocks) {
-    const int4 n = p.starts[c + pieces - 1];
-    if (n.x != b || n.y != sub || n.z == 0) break;
-    ++pieces;
+  for (int k = c + 1;;) {
+    const uint32_t in = __ballot_sync(0xffffffffu, next.x == b && next.y == sub && next.z > 0);
+    const int run = __ffs(~in) - 1;
+    pieces += run < 0 ? 32 : run;
+    if (run >= 0) break;
+    k += 32;
+    next = k + lane < p.blocks ? p.starts[k + lane] : make_int4(-1, 0, 0, 0);
   }
   auto slot = [&](int k) { return (2 * static_cast<int64_t>(c - 1 + k) + (k == 0 ? 1 : 0)) * N + x; };
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
   float M = -INFINITY;
-  for (int k = 0; k < pieces; ++k) M = fmaxf(M, p.part_ml[2 * slot(k)]);
+  for (int k = lane; k < pieces; k += 32) M = fmaxf(M, ml[slot(k)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   const float ref = M == -INFINITY ? 0.f : M;
   float sum = 0.f;
-  for (int k = 0; k < pieces; ++k) sum += ex2(p.part_ml[2 * slot(k)] - ref) * p.part_ml[2 * slot(k) + 1];
+  float4 o[Q];  // columns 4 lane + 128 q ..
+#pragma unroll
+  for (int q = 0; q < Q; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = 0; k0 < pieces; k0 += 32) {
+    float f = 0.f;
+    if (k0 + lane < pieces) {
+      const float2 s = ml[slot(k0 + lane)];
+      f = ex2(s.x - ref);
+      sum = fmaf(f, s.y, sum);
+    }
+    const int n = min(32, pieces - k0);
+#pragma unroll(Q >= 4 ? 2 : 4)
+    for (int k = 0; k < n; ++k) {
+      const float fk = __shfl_sync(0xffffffffu, f, k);
+      const float4* src = reinterpret_cast<const float4*>(p.part_o + slot(k0 + k) * p.D) + lane;
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        if (4 * lane + 128 * q < p.D) {
+          const float4 y = src[32 * q];
+          o[q].x = fmaf(fk, y.x, o[q].x);
+          o[q].y = fmaf(fk, y.y, o[q].y);
+          o[q].z = fmaf(fk, y.z, o[q].z);
+          o[q].w = fmaf(fk, y.w, o[q].w);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const int h = (sub / rt) * p.group + rr / m, i = rr % m;
   typedef typename std::conditional<BF16, __nv_bfloat16, __half>::type T;
   T* orow = static_cast<T*>(p.out) + b * p.o_sb + h * p.o_sh + i * p.o_sn;
-  for (int d = threadIdx.x * 4; d < p.D; d += kMergeThreads * 4) {
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < pieces; ++k) {
-      const float f = ex2(p.part_ml[2 * slot(k)] - ref);
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + slot(k) * p.D + d);
-      o.x = fmaf(f, v.x, o.x);
-      o.y = fmaf(f, v.y, o.y);
-      o.z = fmaf(f, v.z, o.z);
-      o.w = fmaf(f, v.w, o.w);
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    const int d = 4 * lane + 128 * q;
+    if (d < p.D) {
+      uint2 w;
+      w.x = pack2<BF16>(o[q].x * inv, o[q].y * inv);
+      w.y = pack2<BF16>(o[q].z * inv, o[q].w * inv);
+      *reinterpret_cast<uint2*>(orow + d) = w;
     }
-    uint2 w;
-    w.x = pack2<BF16>(o.x * inv, o.y * inv);
-    w.y = pack2<BF16>(o.z * inv, o.w * inv);
-    *reinterpret_cast<uint2*>(orow + d) = w;
   }
   constexpr float kLn2 = 0.6931471805599453f;
-  if (threadIdx.x == 0 && p.lse)
+  if (lane == 0 && p.lse)
     p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.T + i] = sum > 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
 }
 
 template <int N, bool BF16>
-cudaError_t launch_n(const TreeParams& p_in, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
-  TreeParams p = p_in;
-  p.slots = std::min(kMaxSlots, (kMaxSmem - fixed_bytes(p.n_chunks, N)) / kSlotBytes);
-  if (p.slots < 2) return cudaErrorInvalidConfiguration;
-  const int smem = fixed_bytes(p.n_chunks, N) + p.slots * kSlotBytes;
-  auto kern = tree_kernel<N, BF16>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  timing_mark(st);
-  kern<<<p.blocks, tree_threads<N>(), smem, st>>>(mk, mv, p);
-  timing_mark(st);
-  if ((e = cudaGetLastError()) != cudaSuccess || p.blocks < 2) return e;
+cudaError_t launch_merge(const TreeParams& p, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.blocks - 1, N, 1);
+  const int most = std::min(N, p.group * p.T);  // rows of a row tile, at most
+  cfg.gridDim = dim3(p.blocks - 1, (most + kMergeThreads / 32 - 1) / (kMergeThreads / 32), 1);
   cfg.blockDim = dim3(kMergeThreads, 1, 1);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -817,7 +867,23 @@ cudaError_t launch_n(const TreeParams& p_in, const CUtensorMap& mk, const CUtens
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, tree_merge_kernel<N, BF16>, p);
+  if (p.D <= 128) return cudaLaunchKernelEx(&cfg, tree_merge_kernel<N, BF16, 1>, p);
+  if (p.D <= 256) return cudaLaunchKernelEx(&cfg, tree_merge_kernel<N, BF16, 2>, p);
+  if (p.D <= 512) return cudaLaunchKernelEx(&cfg, tree_merge_kernel<N, BF16, 4>, p);
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<N, BF16, 8>, p);
+}
+
+template <int N, bool BF16>
+cudaError_t launch_n(const TreeParams& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
+  const int smem = fixed_bytes(p.n_chunks, N) + p.slots * p.slot_bytes;
+  auto kern = tree_kernel<N, BF16>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  timing_mark(st);
+  kern<<<p.blocks, tree_threads<N>(), smem, st>>>(mk, mv, p);
+  timing_mark(st);
+  if ((e = cudaGetLastError()) != cudaSuccess || p.blocks < 2) return e;
+  e = launch_merge<N, BF16>(p, st);
   timing_mark(st);
   return e;
 }
@@ -827,20 +893,37 @@ cudaError_t launch_tree(const TreeParams& p, const CUtensorMap& mk, const CUtens
   switch (p.rows_n) {
     case 16: return launch_n<16, BF16>(p, mk, mv, st);
     case 32: return launch_n<32, BF16>(p, mk, mv, st);
-    default: return launch_n<64, BF16>(p, mk, mv, st);
+    case 64: return launch_n<64, BF16>(p, mk, mv, st);
+    default: return launch_n<96, BF16>(p, mk, mv, st);
   }
 }
 
 }  // namespace
 
-// Rows per tile: the fewest row tiles, then the smallest N.  O^T takes
-// ceil(D / 128) N columns of TMEM next to 2 N for the scores, so N = 64 serves
-// D <= 768.
-int tree_rows_n(int rows, int D) {
-  const int widest = D <= 768 ? 64 : 32;
-  for (int n = 16; n < widest; n *= 2)
-    if (rows <= n) return n;
-  return widest;
+// The rows of a row tile, the ring and the blocks per SM for `rows` rows per kv head.
+//
+// Rows: the fewest row tiles (each reads K and V again), then the smallest N.
+// O^T takes ceil(D / 128) N columns of TMEM next to the scores, Q and P 2 N D +
+// 1024 N bytes of shared memory next to the ring, so N = 96 serves D <= 512 and
+// N = 64 D <= 768.
+//
+// Two blocks per SM for D <= 256 and N <= 32, where a tile's chain (scores,
+// softmax, product) takes longer than its bytes.
+int tree_shape(TreeParams* p, int64_t rows) {
+  const int widest = p->D <= 512 ? 96 : p->D <= 768 ? 64 : 32;
+  const int64_t tiles = (rows + widest - 1) / widest;
+  int n = widest;
+  for (int c : {64, 32, 16})
+    if (c < widest && (rows + c - 1) / c == tiles) n = c;
+  p->rows_n = n;
+  p->slot_bytes = std::min(2, p->n_chunks) * kChunkBytes;
+  const int fixed = fixed_bytes(p->n_chunks, n);
+  const bool two = p->D <= 256 && n <= 32;
+  // an SM has 228 KB, of which a block's own 1 KB is reserved for the system
+  const int room = two ? (233472 - 2 * 1024) / 2 : kMaxSmem;
+  p->slots = std::min(kMaxSlots, (room - fixed) / p->slot_bytes);
+  p->tmem_cols = two ? 256 : 512;
+  return two ? 2 : 1;
 }
 
 cudaError_t launch_fwd_tree(const TreeParams& p, const CUtensorMap& mk, const CUtensorMap& mv, bool bf16,

@@ -122,14 +122,16 @@ struct TreeParams {
   int page, n_pages, max_pages;
   float scale_log2;
   int rows_n;                 // rows of one row tile: the MMA N
-  int slots;                  // ring slots
+  int slots, slot_bytes;      // ring
+  int tmem_cols;              // TMEM columns per block
   int blocks;                 // blocks of the attention kernel
   float* part_o;              // [2 blocks, rows_n, D] fp32 partials
   float* part_ml;             // [2 blocks, rows_n, 2] their (max, sum), log2 domain
-  int4* starts;               // [blocks] (request or -1, kv head x row tiles + row tile, key tile, 0)
+  int4* starts;               // [blocks] (request or -1, kv head x row tiles + row tile, key tile, drafts)
   uint32_t* status;
 };
-int tree_rows_n(int rows, int D);
+// Sets rows_n, the ring and the TMEM columns; returns the blocks per SM.
+int tree_shape(TreeParams* p, int64_t rows);
 cudaError_t launch_fwd_tree(const TreeParams& p, const CUtensorMap& mk, const CUtensorMap& mv, bool bf16,
                             cudaStream_t s);
 

@@ -223,8 +223,8 @@ int ffpa_bwd_varlen(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_t
  * Nothing behind a request's length is read, so unused rows of its last page
  * may hold anything; the values of drafts that a mask hides must be finite.
  * A missing page (number out of range) counts as zeros.
- * Two launches; fp32 partials of at most 2 rows_n D floats per SM (rows_n 16,
- * 32 or 64) in stream-ordered scratch.
+ * Two launches; fp32 partials of at most 2 n D floats per block (n rows, 16 to
+ * 96; one block per SM, two for D <= 256) in stream-ordered scratch.
  */
 int ffpa_fwd_tree(const ffpa_tensor_t* q, const ffpa_tensor_t* k_cache, const ffpa_tensor_t* v_cache,
                   const int32_t* block_table, int max_pages, const int32_t* seq_lens, const int32_t* draft_lens,
