@@ -710,7 +710,7 @@ int fwd_tree_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* kc, const ffpa_te
   p.max_pages = max_pages;
   p.scale_log2 = scale * kLog2e;
   const int64_t rows = static_cast<int64_t>(p.group) * p.T;
-  const int most = tree_shape(&p, rows) * sms;
+  const int most = tree_shape(&p, rows, dtype_is_bf16(c.dtype)) * sms;
   // as many blocks as there can be key tiles to share out
   const int64_t units = c.B * c.Hkv * ((rows + p.rows_n - 1) / p.rows_n);
   const int64_t tiles = (static_cast<int64_t>(max_pages) * p.page + kTileRows - 1) / kTileRows;

@@ -29,9 +29,12 @@
 // read.  Boxes past the length, and pages with a bad number, use a page index
 // out of range: zeros.  The scores of such rows are -inf.
 //
-// P goes to shared memory as two terms of the input type, the rounded weight
-// and its rounding residual, each with its own product: the matrix pipe has
-// the time, and O then carries P to about 2^-16.
+// bf16 P goes to shared memory as two terms, the rounded weight and its rounding
+// residual, each with its own product: for N <= 64 the matrix pipe has the
+// time (an MMA of these shapes takes 46 to 57 cycles, 64 of them per V tile of D =
+// 512, against 10,000 cycles for the tile's bytes), and O then carries P to
+// about 2^-16.  At N = 96 the residual's 24 KB are worth more as a third ring
+// slot, and fp16 weights, rounded to 2^-11, need none.
 //
 // Warps: 0 and 2 TMA producers (alternate ring slots; the lanes of a warp issue
 // a slot's boxes), 1 TMEM owner and MMA issuer, from 4 on softmax, correction
@@ -46,8 +49,10 @@
 namespace ffpa {
 namespace {
 
-// P of a key tile: two halves of 64 keys, each N rows of 128 bytes
+// P of a key tile: two halves of 64 keys, each N rows of 128 bytes; and as much
+// again for the rounding residual where it is kept.
 constexpr int p_bytes(int N) { return 2 * N * 128; }
+constexpr bool keeps_residual(int N, bool bf16) { return bf16 && N <= 64; }
 constexpr int kMaxSlots = 6;
 constexpr int kMaxSmem = 232448;
 constexpr float kRescaleLog2 = 8.0f;  // rescale O only when a row's max grows by > 2^8
@@ -190,8 +195,11 @@ constexpr int kMiscBytes = 256 /* barriers, TMEM base, start */ + 128 /* work su
                            96 * 8 * 2 /* rows in out and lse */ + 12 * 32 * 4 * 2 /* statistics */;
 static_assert(kMiscBytes % 128 == 0, "tile alignment");
 __host__ __device__ constexpr int q_bytes(int n_chunks, int N) { return n_chunks * N * 128; }
-__host__ __device__ constexpr int fixed_bytes(int n_chunks, int N) {
-  return q_bytes(n_chunks, N) + 2 * p_bytes(N) + kMiscBytes + 1024;
+__host__ __device__ constexpr int fixed_bytes(int n_chunks, int N, bool bf16) {
+  // D = 64: a V slot holds one chunk, and the second half of its M = 128 operand
+  // is the 16 KB after it, past the ring for the last slot
+  return q_bytes(n_chunks, N) + (keeps_residual(N, bf16) ? 2 : 1) * p_bytes(N) + kMiscBytes + 1024 +
+         (n_chunks == 1 ? kChunkBytes : 0);
 }
 
 template <bool BF16>
@@ -306,20 +314,21 @@ __global__ void __launch_bounds__(tree_threads<N>(), tree_residency<N>())
   constexpr int kSoftWarps = kThreads / 32 - 4;
   constexpr int C = N < 32 ? N : 32;       // rows per softmax thread
   constexpr int kSBuf = N == 96 ? 1 : 2;   // S^T buffers: TMEM has room for one next to a 96-row O^T
+  constexpr bool kLo = keeps_residual(N, BF16);
   constexpr Bars bl = bar_layout();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int NC = p.n_chunks, slots = p.slots;
   const uint32_t slot_bytes = p.slot_bytes;
   const uint32_t ring = smem_u32(smem), p_hi = ring + slots * slot_bytes, p_lo = p_hi + p_bytes(N);
-  const uint32_t q_sm = p_lo + p_bytes(N);
-  uint8_t* misc = smem + slots * slot_bytes + 2 * p_bytes(N) + q_bytes(NC, N);
+  const uint32_t q_sm = kLo ? p_lo + p_bytes(N) : p_lo;
+  uint8_t* misc = smem + slots * slot_bytes + (kLo ? 2 : 1) * p_bytes(N) + q_bytes(NC, N);
   uint64_t* bars = reinterpret_cast<uint64_t*>(misc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + bl.count);
   Walk<N>* start = reinterpret_cast<Walk<N>*>(misc + 176);  // the block's first segment (left == 0: none)
   int64_t* sums = reinterpret_cast<int64_t*>(misc + 256);
   uint32_t* vis = reinterpret_cast<uint32_t*>(misc + 256 + 128);       // [3][128] draft -> rows that see it, 32 rows each
-  int64_t* row_off = reinterpret_cast<int64_t*>(vis + 3 * 128);        // [N] offset of the row in out, -1: padding
+  int64_t* row_off = reinterpret_cast<int64_t*>(vis + 3 * 128);        // [N] offset of the row in out (0: padding)
   int64_t* row_lse = row_off + 96;                                     // [N] index of the row in lse
   float* stat = reinterpret_cast<float*>(row_lse + 96);                // [warps][32] exchanged statistics
   float* bcast = stat + 12 * 32;                                       // [warps][32] per-row values of one warp
@@ -502,9 +511,10 @@ __global__ void __launch_bounds__(tree_threads<N>(), tree_residency<N>())
           for (int ks = 0; ks < 8; ++ks)
             umma_ss(d, sdesc_advance(a, ks * 2048), sdesc_advance(dhi, (ks >> 2) * (N * 128) + (ks & 3) * 32), idesc_o,
                     t > w.tile || ks > 0);
+          if constexpr (kLo)
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            umma_ss(d, sdesc_advance(a, ks * 2048), sdesc_advance(dlo, (ks >> 2) * (N * 128) + (ks & 3) * 32), idesc_o,
+            for (int ks = 0; ks < 8; ++ks)
+              umma_ss(d, sdesc_advance(a, ks * 2048), sdesc_advance(dlo, (ks >> 2) * (N * 128) + (ks & 3) * 32), idesc_o,
                     1u);
           umma_commit(bar(bl.empty + s));
         }
@@ -538,7 +548,7 @@ __global__ void __launch_bounds__(tree_threads<N>(), tree_residency<N>())
       if (!bar_and(4, kAll, ok)) break;  // the epilogue before has read the tables
       if (st < N) {
         const int rr = w.row0 + st;
-        int64_t off = -1;
+        int64_t off = 0;
         int64_t li = 0;
         if (rr < rows) {
           const int h = w.hk * p.group + rr / m, i = rr % m;
@@ -693,14 +703,16 @@ __global__ void __launch_bounds__(tree_threads<N>(), tree_residency<N>())
             l[x + u] += e[u];
             l[x + u + 1] += e[u + 1];
             const uint32_t hi = pack2<BF16>(e[u], e[u + 1]);
-            const float2 r = unpack2<BF16>(hi);
-            const uint32_t lo = pack2<BF16>(e[u] - r.x, e[u + 1] - r.y);
             const uint32_t at0 = key_at + (x + u) * 128 + ((gran ^ ((x + u) & 7)) << 4);
             const uint32_t at1 = key_at + (x + u + 1) * 128 + ((gran ^ ((x + u + 1) & 7)) << 4);
             st_shared_u16(p_hi + at0, hi);
             st_shared_u16(p_hi + at1, hi >> 16);
-            st_shared_u16(p_lo + at0, lo);
-            st_shared_u16(p_lo + at1, lo >> 16);
+            if constexpr (kLo) {
+              const float2 r = unpack2<BF16>(hi);
+              const uint32_t lo = pack2<BF16>(e[u] - r.x, e[u + 1] - r.y);
+              st_shared_u16(p_lo + at0, lo);
+              st_shared_u16(p_lo + at1, lo >> 16);
+            }
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -715,6 +727,7 @@ __global__ void __launch_bounds__(tree_threads<N>(), tree_residency<N>())
       ok = bar_and(nb, 128, ok);
       const float sum = (wg_stat[lane] + wg_stat[32 + lane]) + (wg_stat[64 + lane] + wg_stat[96 + lane]);
       tc_fence_after();
+      const int mine = rows - w.row0 - wg * C;  // of this warpgroup's rows, those that are not padding
       if (w.whole()) {
         my_bcast[lane] = sum > 0.f ? 1.f / sum : 0.f;
         __syncwarp();
@@ -725,16 +738,16 @@ __global__ void __launch_bounds__(tree_threads<N>(), tree_residency<N>())
           if (d < p.D) {
 #pragma unroll
             for (int x = 0; x < C; ++x) {
-              const int64_t off = row_off[wg * C + x];
-              if (off >= 0) store1<BF16>(p.out, off + d, __uint_as_float(v[x]) * my_bcast[x]);
+              const int64_t off = row_off[wg * C + x] + d;
+              const float y = __uint_as_float(v[x]) * my_bcast[x];
+              if (x < mine) store1<BF16>(p.out, off, y);
             }
           }
         }
-        if ((warp & 3) == 0 && lane < C && p.lse && row_off[wg * C + lane] >= 0)
+        if ((warp & 3) == 0 && lane < C && p.lse && lane < mine)
           p.lse[row_lse[wg * C + lane]] = sum > 0.f ? (m_used + __log2f(sum)) * kLn2 : -INFINITY;
       } else {
         const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (w.tile > 0 ? 0 : 1);
-        const int mine = rows - w.row0 - wg * C;  // of this warpgroup's rows, those that are not padding
         float* part = p.part_o + (slot * N + wg * C) * p.D;
         for (int blk = 0; blk < kslots; ++blk) {
           uint32_t v[C];
@@ -875,7 +888,7 @@ cudaError_t launch_merge(const TreeParams& p, cudaStream_t st) {
 
 template <int N, bool BF16>
 cudaError_t launch_n(const TreeParams& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
-  const int smem = fixed_bytes(p.n_chunks, N) + p.slots * p.slot_bytes;
+  const int smem = fixed_bytes(p.n_chunks, N, BF16) + p.slots * p.slot_bytes;
   auto kern = tree_kernel<N, BF16>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -909,7 +922,7 @@ cudaError_t launch_tree(const TreeParams& p, const CUtensorMap& mk, const CUtens
 //
 // Two blocks per SM for D <= 256 and N <= 32, where a tile's chain (scores,
 // softmax, product) takes longer than its bytes.
-int tree_shape(TreeParams* p, int64_t rows) {
+int tree_shape(TreeParams* p, int64_t rows, bool bf16) {
   const int widest = p->D <= 512 ? 96 : p->D <= 768 ? 64 : 32;
   const int64_t tiles = (rows + widest - 1) / widest;
   int n = widest;
@@ -917,7 +930,7 @@ int tree_shape(TreeParams* p, int64_t rows) {
     if (c < widest && (rows + c - 1) / c == tiles) n = c;
   p->rows_n = n;
   p->slot_bytes = std::min(2, p->n_chunks) * kChunkBytes;
-  const int fixed = fixed_bytes(p->n_chunks, n);
+  const int fixed = fixed_bytes(p->n_chunks, n, bf16);
   const bool two = p->D <= 256 && n <= 32;
   // an SM has 228 KB, of which a block's own 1 KB is reserved for the system
   const int room = two ? (233472 - 2 * 1024) / 2 : kMaxSmem;

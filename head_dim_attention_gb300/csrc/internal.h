@@ -131,7 +131,7 @@ struct TreeParams {
   uint32_t* status;
 };
 // Sets rows_n, the ring and the TMEM columns; returns the blocks per SM.
-int tree_shape(TreeParams* p, int64_t rows);
+int tree_shape(TreeParams* p, int64_t rows, bool bf16);
 cudaError_t launch_fwd_tree(const TreeParams& p, const CUtensorMap& mk, const CUtensorMap& mv, bool bf16,
                             cudaStream_t s);
 
