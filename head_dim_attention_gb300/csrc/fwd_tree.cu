@@ -232,6 +232,10 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
 __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
   asm volatile("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tst.shared.b16 [%0], h;\n\t}" ::"r"(addr), "r"(v) : "memory");
 }
+// Asynchronous 16-byte copy to shared memory; zeros where `real` is false.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
 // All `threads` threads meet; true if every one of them passes true.
 __device__ __forceinline__ bool bar_and(uint32_t id, uint32_t threads, bool v) {
   uint32_t r;
@@ -541,10 +545,34 @@ __global__ void __launch_bounds__(tree_threads<N>(), tree_residency<N>())
     constexpr float kLn2 = 0.6931471805599453f;
     bool ok = true;
     uint32_t tc = 0;
-    Walk<N> w = *start;
-    do {
+    // Q rows of a row tile, K-major with the 128-byte swizzle, padding rows zero:
+    // warp sw copies rows sw, sw + kSoftWarps, ..; the copies are asynchronous
+    auto issue_q = [&](const Walk<N>& w) {
+      const int m = w.r.m;
+      for (int r = sw; r < N; r += kSoftWarps) {
+        const int rr = w.row0 + r;
+        const bool real = rr < p.group * m;
+        const uint4* src = reinterpret_cast<const uint4*>(p.q);
+        if (real)
+          src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + w.b * p.q_sb +
+                                               (w.hk * p.group + rr / m) * p.q_sh + (rr % m) * p.q_sn);
+        for (int gq = lane; gq < 8 * NC; gq += 32)
+          cp_async16(q_sm + (gq >> 3) * (N * 128) + r * 128 + (((gq & 7) ^ (r & 7)) << 4), real ? src + gq : src, real);
+      }
+    };
+    auto finish_q = [&]() {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bl.q_full));
+    };
+    Walk<N> w = *start, after = w;
+    bool more = true;
+    issue_q(w);
+    finish_q();
+    while (more) {
       const int m = w.r.m, n = w.r.n, prefix = n - m, rows = p.group * m;
-      // ---- the unit: row offsets, draft visibility, Q
+      // ---- the unit: row offsets, draft visibility (its Q is on the way)
       if (!bar_and(4, kAll, ok)) break;  // the epilogue before has read the tables
       if (st < N) {
         const int rr = w.row0 + st;
@@ -573,42 +601,6 @@ __global__ void __launch_bounds__(tree_threads<N>(), tree_residency<N>())
           vis[g * 128 + j] = bits;
         }
       }
-      // Q rows of the tile, K-major with the 128-byte swizzle; padding rows zero.
-      // A warp takes rows sw, sw + kSoftWarps, ..: four at a time, two 16-byte
-      // granules of each per lane, all in flight together.
-      for (int r0 = sw; r0 < N; r0 += 4 * kSoftWarps) {
-        const uint4* src[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int rr = w.row0 + r0 + u * kSoftWarps;
-          src[u] = nullptr;
-          if (rr < rows)
-            src[u] = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + w.b * p.q_sb +
-                                                    (w.hk * p.group + rr / m) * p.q_sh + (rr % m) * p.q_sn);
-        }
-        for (int g0 = lane; g0 < 8 * NC; g0 += 64) {
-          uint4 x[4][2];
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              x[u][e] = make_uint4(0u, 0u, 0u, 0u);
-              if (src[u] && g0 + 32 * e < 8 * NC) x[u][e] = __ldg(src[u] + g0 + 32 * e);
-            }
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int r = r0 + u * kSoftWarps, gq = g0 + 32 * e;
-              if (r < N && gq < 8 * NC)
-                st_shared_v4(q_sm + (gq >> 3) * (N * 128) + r * 128 + (((gq & 7) ^ (r & 7)) << 4), x[u][e].x,
-                             x[u][e].y, x[u][e].z, x[u][e].w);
-            }
-        }
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(bl.q_full));
       if (!bar_and(4, kAll, ok)) break;  // tables written
 
       float l[C];  // this key's share of the rows' sums
@@ -720,11 +712,17 @@ __global__ void __launch_bounds__(tree_threads<N>(), tree_residency<N>())
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(bl.p_ready));
       }
-      // ---- the unit's end: row sums, then O^T to out or to a partial
+      // ---- the unit's end: row sums, then O^T to out or to a partial.  Every
+      // score of the unit has been computed, so the next unit's Q may replace
+      // this one's while the last product runs.
+      after = w;
+      more = after.next(p);
+      if (more) issue_q(after);
       if (ok) ok = mbar_wait<false>(bar(bl.pv_done), (tc - 1) & 1, status);
       ok = __all_sync(0xffffffffu, ok);
       my_stat[lane] = reduce_columns<C>(l, lane, SumOp());
       ok = bar_and(nb, 128, ok);
+      if (more) finish_q();
       const float sum = (wg_stat[lane] + wg_stat[32 + lane]) + (wg_stat[64 + lane] + wg_stat[96 + lane]);
       tc_fence_after();
       const int mine = rows - w.row0 - wg * C;  // of this warpgroup's rows, those that are not padding
@@ -768,7 +766,8 @@ __global__ void __launch_bounds__(tree_threads<N>(), tree_residency<N>())
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(bl.o_free));
-    } while (w.next(p));
+      w = after;
+    }
   }
 
   tc_fence_before();
