@@ -149,9 +149,8 @@ def cache_plan(lens, new_lens, block_table, free_pages, free_head, page_size, ma
     one), lens_out and free_head_out; lens and free_head themselves may be
     given for the last two."""
     import torch
-    i32 = dict(dtype=torch.int32, device=lens.device)
-    cu_new = torch.empty(lens.shape[0] + 1, **i32) if cu_new is None else cu_new
-    slots = torch.empty(max_new, dtype=torch.int64, device=lens.device) if slots is None else slots
+    cu_new = lens.new_empty(lens.shape[0] + 1) if cu_new is None else cu_new
+    slots = lens.new_empty(max_new, dtype=torch.int64) if slots is None else slots
     if slots.shape[0] != max_new:
         raise ValueError(f"slots must have max_new = {max_new} entries, got {slots.shape[0]}")
     lens_out = torch.empty_like(lens) if lens_out is None else lens_out

@@ -75,11 +75,25 @@ def test_varlen_bwd_needs_everything(lib, name):
 
 
 def test_binding_checks_integer_tensors():
-    ok = torch.zeros(4, dtype=torch.int32)
-    _lib._ints(ok, "cu_seqlens", 1)
+    _lib._ints(torch.zeros(4, dtype=torch.int32), "cu_seqlens", (-1,))
+    _lib._ints(torch.zeros(2, 3, dtype=torch.int32), "block_table", (2, -1))
     for bad in (torch.zeros(4, dtype=torch.int64), torch.zeros(2, 2, dtype=torch.int32), torch.zeros(8, dtype=torch.int32)[::2]):
         with pytest.raises(ValueError, match="cu_seqlens"):
-            _lib._ints(bad, "cu_seqlens", 1)
+            _lib._ints(bad, "cu_seqlens", (-1,))
+    with pytest.raises(ValueError, match="seq_lens"):
+        _lib._ints(torch.zeros(4, dtype=torch.int32), "seq_lens", (5,))
+
+
+def test_packed_descriptors_are_the_described_ones():
+    for t in (torch.zeros(2, 3, 5, 64, dtype=torch.bfloat16), torch.zeros(3, 5, 64, dtype=torch.float16).transpose(0, 1)[None]):
+        got = _lib.FfpaTensor.from_buffer_copy(_lib._pack(t))
+        assert (got.data, got.dtype, got.reserved) == (t.data_ptr(), _lib._dtype_code(t), 0)
+        assert tuple(got.shape) == tuple(t.shape) and tuple(got.stride) == t.stride()
+    lse = _lib.FfpaTensor.from_buffer_copy(_lib._pack_lse(torch.zeros(2, 3, 5)))
+    assert tuple(lse.shape) == (2, 3, 5, 1) and tuple(lse.stride) == (15, 5, 1, 1)
+    assert _lib._pack_lse(None) is None
+    with pytest.raises(ValueError, match="4-D"):
+        _lib._pack(torch.zeros(2, 3, 64))
 
 
 # ------------------------------------------------------------------ paged cache
