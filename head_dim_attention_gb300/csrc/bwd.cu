@@ -601,6 +601,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               pv[c4 * 32 + e] = ex2(fmaf(f[e], p.scale_log2, -l2));
             }
           }
+        } else if constexpr (VAR) {
+          const VarSpan in = var_span<MODE == kDQ>(p, srow, cr0);
+#pragma unroll
+          for (int c4 = 0; c4 < 4; ++c4) {
+            float f[32];
+            chunk(kX1, c4, f);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const int ci = c4 * 32 + e;
+              const float l2 = (MODE == kDQ) ? lse2_row : __shfl_sync(0xffffffffu, l2v[c4], e);
+              const float x = ex2(fmaf(f[e], p.scale_log2, -var_lse(l2)));
+              pv[ci] = ci >= in.lo && ci < in.hi ? x : 0.f;
+            }
+          }
         } else {
 #pragma unroll
         for (int c4 = 0; c4 < 4; ++c4) {

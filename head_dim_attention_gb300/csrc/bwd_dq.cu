@@ -438,6 +438,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (plain) {
 #pragma unroll
         for (int e = 0; e < 64; ++e) pv[e] = ex2(fmaf(pv[e], p.scale_log2, -lse2_row));
+      } else if constexpr (VAR) {
+        const VarSpan in = var_span<true>(p, srow, cbase);
+#pragma unroll
+        for (int e = 0; e < 64; ++e) {
+          const float x = ex2(fmaf(pv[e], p.scale_log2, -var_lse(lse2_row)));
+          pv[e] = e < in.hi ? x : 0.f;
+        }
       } else {
 #pragma unroll
         for (int e = 0; e < 64; ++e) {

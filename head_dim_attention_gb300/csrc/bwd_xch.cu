@@ -645,6 +645,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (plain) {
 #pragma unroll
           for (int e = 0; e < 64; ++e) xv[e] = ex2(fmaf(xv[e], p.scale_log2, -stat(e)));
+        } else if constexpr (VAR) {
+          const VarSpan in = var_span<DQ>(p, srow, cbase);
+#pragma unroll
+          for (int e = 0; e < 64; ++e) {
+            const float x = ex2(fmaf(xv[e], p.scale_log2, -var_lse(stat(e))));
+            xv[e] = e >= in.lo && e < in.hi ? x : 0.f;
+          }
         } else {
 #pragma unroll
           for (int e = 0; e < 64; ++e) {

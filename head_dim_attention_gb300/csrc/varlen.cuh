@@ -67,6 +67,23 @@ __device__ __forceinline__ void localize(BwdParams& p, const VarTile& t) {
   p.lse2 += t.start;
 }
 
+// The backward's masked tiles.  With a bias and 64-bit addresses in it, the general
+// per-score code of a masked 128 x 128 tile takes about 8 us (D = 64, 14,000 cycles
+// for a thread's 128 scores), which short sequences pay on nearly every tile.  A
+// packed call has no bias, and its masks leave one span of a thread's scores:
+// those of columns base + lo .. base + hi - 1.
+struct VarSpan {
+  int lo, hi;
+};
+// Stationary row `srow` is a query (DQ) or a key; the columns are the other side.
+template <bool DQ>
+__device__ __forceinline__ VarSpan var_span(const BwdParams& p, int srow, int base) {
+  if (DQ) return {0, srow < p.Nq ? (p.causal ? min(p.Nkv, srow + 1) : p.Nkv) - base : 0};
+  return {p.causal ? srow - base : 0, srow < p.Nkv ? p.Nq - base : 0};
+}
+// A row without keys has lse -inf and no weights: 2^(x - inf) = 0.
+__device__ __forceinline__ float var_lse(float l2) { return l2 == -INFINITY ? INFINITY : l2; }
+
 // Distance between the heads of lse, delta and lse2.
 template <bool VAR, class P>
 __device__ __forceinline__ int stat_rows(const P& p) {
