@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(256) bwd_preprocess_kernel(const __grid_consta
   const int64_t rows = static_cast<int64_t>(p.B) * p.Hq * p.Nq;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
+  if (p.var.tiles) var_end();  // beside the plan, which ends first
   if (row >= rows) return;
   const int i = static_cast<int>(row % p.Nq);
   const int h = static_cast<int>((row / p.Nq) % p.Hq);
@@ -198,8 +199,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   VarTile vt = {};
   BwdParams p_var;
   if constexpr (VAR) {
+    var_start();
     vt = var_tile(p_in.var, static_cast<int>(blockIdx.x));
-    if (vt.seq < 0) return;  // an empty slot
+    if (vt.seq < 0) {  // an empty slot
+      var_end();
+      return;
+    }
     p_var = p_in;
     localize(p_var, vt);
   }
@@ -746,6 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tbase, kTmemCols);
   }
+  if constexpr (VAR) var_end();
 }
 
 template <int MODE, bool BF16>
@@ -780,6 +786,9 @@ cudaError_t launch_mode(const BwdParams& p_in, const BwdMaps& m, cudaStream_t st
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  cfg.attrs = attr;
+  if (p.var.tiles && MODE != kDV) set_overlap(&attr[cfg.numAttrs++]);
   e = cudaLaunchKernelEx(&cfg, kern, m.q, m.k, m.v, m.dout, p, n_res);
   timing_mark(st);
   return e;
@@ -789,9 +798,16 @@ template <bool BF16>
 cudaError_t launch_preprocess(const BwdParams& p, cudaStream_t st) {
   const int64_t rows = static_cast<int64_t>(p.B) * p.Hq * p.Nq;
   timing_mark(st);
-  bwd_preprocess_kernel<BF16><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, st>>>(p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8), 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  cfg.attrs = attr;
+  if (p.var.tiles) set_overlap(&attr[cfg.numAttrs++]);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, bwd_preprocess_kernel<BF16>, p);
   timing_mark(st);
-  return cudaGetLastError();
+  return e;
 }
 
 template <bool BF16>

@@ -144,7 +144,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   BwdParams p_var;
   if constexpr (VAR) {
     vt = var_tile(p_in.var, static_cast<int>(blockIdx.x) >> 1);
-    if (vt.seq < 0) return;  // an empty slot (the whole cluster's)
+    if (vt.seq < 0) {  // an empty slot (the whole cluster's)
+      var_end();
+      return;
+    }
     p_var = p_in;
     localize(p_var, vt);
   }
@@ -557,6 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc_pair(tbase, kTmemCols);
   }
+  if constexpr (VAR) var_end();
 }
 
 template <int NC, bool BF16>
@@ -574,13 +578,14 @@ cudaError_t launch_impl(const BwdParams& p, const BwdMaps& m, cudaStream_t st) {
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (p.var.tiles) set_overlap(&attr[cfg.numAttrs++]);
   e = cudaLaunchKernelEx(&cfg, kern, m.k, m.q_half, m.k_half, m.v_half, m.dout_half, p);
   timing_mark(st);
   return e;

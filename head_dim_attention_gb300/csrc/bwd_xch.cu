@@ -234,8 +234,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   VarTile vt = {};
   BwdParams p_var;
   if constexpr (VAR) {
+    var_start();
     vt = var_tile(p_in.var, (static_cast<int>(blockIdx.x) >> 2) / (MODE == kDKV ? G::kSplitKV : 1));
-    if (vt.seq < 0) return;  // an empty slot (the whole cluster's)
+    if (vt.seq < 0) {  // an empty slot (the whole cluster's)
+      var_end();
+      return;
+    }
     p_var = p_in;
     localize(p_var, vt);
   }
@@ -541,18 +545,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const uint4* srow_ptr = reinterpret_cast<const uint4*>(base + g.b * sb + g.hs * sh +
                                                              static_cast<int64_t>(min(srow, g.s_limit - 1)) * sn);
+      // kBatch chunks' loads are in flight together (packed sequences: this round
+      // trip is a large part of a short sequence's tile)
+      constexpr int kBatch = VAR ? 4 : 1;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t wv[32];
+      for (int c0 = 0; c0 < 4; c0 += kBatch) {
+        uint32_t wv[kBatch][32];
 #pragma unroll
-        for (int gq = 0; gq < 8; ++gq) {
-          const uint4 x = __ldg(srow_ptr + 8 * c + gq);
-          wv[4 * gq] = x.x;
-          wv[4 * gq + 1] = x.y;
-          wv[4 * gq + 2] = x.z;
-          wv[4 * gq + 3] = x.w;
-        }
-        tmem_st32(tbase + lane_off + kSt + 32 * c, wv);
+        for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+          for (int gq = 0; gq < 8; ++gq) {
+            const uint4 x = __ldg(srow_ptr + 8 * (c0 + k) + gq);
+            wv[k][4 * gq] = x.x;
+            wv[k][4 * gq + 1] = x.y;
+            wv[k][4 * gq + 2] = x.z;
+            wv[k][4 * gq + 3] = x.w;
+          }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) tmem_st32(tbase + lane_off + kSt + 32 * (c0 + k), wv[k]);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -825,6 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc_pair(tbase, kTmemCols);
   }
+  if constexpr (VAR) var_end();
 }
 
 template <int MODE, int NC, bool BF16>
@@ -842,13 +853,14 @@ cudaError_t launch_impl(const BwdParams& p, const BwdMaps& m, cudaStream_t st) {
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 4;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (p.var.tiles && MODE == kDQ) set_overlap(&attr[cfg.numAttrs++]);
   e = cudaLaunchKernelEx(&cfg, kern, m.q_half, m.k_half, m.v_half, m.dout_half, p);
   timing_mark(st);
   return e;

@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   VarTile vt = {};
   FwdParams p_var;
   if constexpr (VAR) {
+    var_wait();
     vt = var_tile(p_in.var, static_cast<int>(blockIdx.x));
     if (vt.seq < 0) return;  // an empty slot
     p_var = p_in;
@@ -542,6 +543,9 @@ cudaError_t launch_impl(const FwdParams& p_in, const FwdMaps& m, cudaStream_t st
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  cfg.attrs = attr;
+  if (p.var.tiles) set_overlap(&attr[cfg.numAttrs++]);
   timing_mark(st);
   e = cudaLaunchKernelEx(&cfg, kern, m.q, m.k, m.v, p);
   timing_mark(st);

@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   VarTile vt = {};
   FwdParams p_var;
   if constexpr (VAR) {
+    var_wait();
     vt = var_tile(p_in.var, static_cast<int>(blockIdx.x >> 2));
     if (vt.seq < 0) return;  // an empty slot (the whole cluster's)
     p_var = p_in;
@@ -704,13 +705,14 @@ cudaError_t launch_impl(const FwdParams& p_in, const FwdMaps& m, cudaStream_t st
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 4;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (p.var.tiles) set_overlap(&attr[cfg.numAttrs++]);
   timing_mark(st);
   e = cudaLaunchKernelEx(&cfg, kern, m.q_half, m.k_half, m.v, p);
   timing_mark(st);

@@ -213,6 +213,11 @@ struct BwdMaps {
 
 bool dtype_is_bf16(int dtype);
 
+// Launch attribute of a kernel that may start before the one ahead of it in the stream has ended (varlen.cuh).
+inline void set_overlap(cudaLaunchAttribute* attr) {
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
+}
 // Fills the tile slots and the per-sequence maps of a packed call (varlen.cu).
 cudaError_t launch_varlen_plan(const VarPlan& p, cudaStream_t s);
 

@@ -34,6 +34,7 @@ __device__ __forceinline__ SeqRange seq_range(const VarPlan& p, int s) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) varlen_plan_kernel(const __grid_constant__ VarPlan p) {
+  var_start();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kWarps = kPlanThreads / 32;
   if (blockIdx.x > 0) {

@@ -26,6 +26,21 @@ struct VarTile {
   int start, len;
 };
 
+// A packed call's launches overlap where they do not depend on one another (each is
+// launched as a programmatic dependent of the one before):
+//   forward   the attention kernel starts while the plan runs and waits for it
+//             (var_wait) before it reads its tile;
+//   backward  the preprocess runs beside the plan; the first gradient kernel follows
+//             both; the others read nothing of its results, so they start as its
+//             blocks leave.  The last block of each ends only after the launch
+//             before has (var_end), so that the end of the last launch is the end
+//             of all: one block, because a block that waits holds its SM.
+__device__ __forceinline__ void var_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void var_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void var_end() {
+  if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1) var_wait();
+}
+
 __device__ __forceinline__ VarTile var_tile(const VarParams& v, int slot) {
   const int4 t = __ldg(v.tiles + slot);
   return VarTile{t.x, t.y, t.z, t.w};
