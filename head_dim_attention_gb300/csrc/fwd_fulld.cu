@@ -111,11 +111,11 @@ struct Shape {
 };
 
 struct Bars {
-  int full_k, empty_k, full_v, empty_v, q_full, s_full, s_free, p_ready, p_local, pv_done, drain_a, drain_b, count;
+  int full_k, empty_k, full_v, empty_v, q_full, s_full, s_free, p_ready, p_local, pv_done, drain_a, drain_b, q_stage, count;
 };
 // s_full, s_free: one per TMEM score buffer; p_ready, p_local, pv_done: one per P buffer
 __host__ __device__ constexpr Bars bar_layout() {
-  return Bars{0, 2, 4, 6, 8, 9, 11, 13, 15, 17, 19, 20, 21};
+  return Bars{0, 2, 4, 6, 8, 9, 11, 13, 15, 17, 19, 20, 21, 22};
 }
 static_assert(bar_layout().count * 8 + 16 <= 256, "barrier area");
 
@@ -150,6 +150,20 @@ __device__ __forceinline__ void store_row64(uint32_t tile, int r, const uint32_t
   for (int g = 0; g < 8; ++g)
     st_shared_v4(row + ((static_cast<uint32_t>(g) ^ static_cast<uint32_t>(r & 7)) << 4), w[4 * g], w[4 * g + 1],
                  w[4 * g + 2], w[4 * g + 3]);
+}
+
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(addr) : "memory");
+}
+// Named barrier of the four softmax warps; true if all of them pass true.
+__device__ __forceinline__ bool all_bar_and(uint32_t id, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(v)), "r"(id)
+      : "memory");
+  return r != 0;
 }
 
 // Named barrier of the two softmax warps that hold the two key halves of the
@@ -245,6 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(bl.q_full), 1 + 8);
     mbar_init(bar(bl.drain_a), 1);
     mbar_init(bar(bl.drain_b), 1);
+    mbar_init(bar(bl.q_stage), 1);
     lo_flag[0] = 0;
     lo_flag[1] = 0;
     fence_mbar_init();
@@ -280,7 +295,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_load_4d_pair(q_sm + (c - kQtc) * kHalfBytes, m_qh, lead(bl.q_full), c * kChunk,
                          q0 + 64 * static_cast<int>(rank), h, b);
     } else {
-      if constexpr (VAR) var_map_acquire(m_v);
+      if constexpr (VAR) {
+        var_map_acquire(m_qh);
+        // Q's first kQtc chunks of this CTA's 64 rows, for the softmax warps (below)
+        mbar_expect_tx(bar(bl.q_stage), kQtc * kHalfBytes);
+        for (int c = 0; c < kQtc; ++c)
+          tma_load_4d(p_sm + c * kHalfBytes, m_qh, bar(bl.q_stage), c * kChunk, q0 + 64 * static_cast<int>(rank), h, b);
+        var_map_acquire(m_v);
+      }
       tma_prefetch_desc(m_v);
     }
     bool ok = true;
@@ -425,33 +447,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr float kLog2e = 1.4426950408889634f;
     const uint32_t s_free_lead0 = lead(bl.s_free), s_free_lead1 = lead(bl.s_free + 1);
     const uint32_t p_ready_local = bar(rank == 0 ? bl.p_ready : bl.p_local);  // + 8 per P buffer
-    {
+    if constexpr (VAR) {
+      // The same rows by way of the P buffers, idle until the first score: read row by
+      // row from global memory, every load and store of a warp touches 32 lines, which
+      // took 3.3 us at the start of a tile (and 2.4 us for O at its end, below), where
+      // a short sequence's tile takes 10 us in all.
+      static_assert(kQtc * kHalfBytes <= kNpb * kPBufBytes && 64 * G::kOw * 2 <= kNpb * kPBufBytes,
+                    "Q's and O's rows fit the P buffers");
+      mbar_wait<false>(bar(bl.q_stage), 0, status);
+#pragma unroll
+      for (int c = 0; c < kQtc; ++c) {
+        uint32_t w[32];
+#pragma unroll
+        for (int g = 0; g < 8; ++g)
+          ld_shared_v4(p_sm + c * kHalfBytes + r * 128 + ((g ^ (r & 7)) << 4), w[4 * g], w[4 * g + 1], w[4 * g + 2],
+                       w[4 * g + 3]);
+        tmem_st32(tbase + lane_off + kQt + 32 * c, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0)
+          mbar_arrive(bar(bl.q_full));
+        else
+          mbar_arrive_remote(lead(bl.q_full));
+      }
+    } else {
       // Q columns 0 .. 64 kQtc - 1 of this thread's row into its TMEM lane: words of
       // two 16-bit values in memory order, the TS form's A layout (the threads of
       // lanes r and r + 64 write the same row)
       typedef typename std::conditional<BF16, __nv_bfloat16, __half>::type T;
       const uint4* qrow = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.q) + b * p.q_sb + h * p.q_sh +
                                                          static_cast<int64_t>(min(row, p.Nq - 1)) * p.q_sn);
-      // kBatch chunks' loads are in flight together: short packed sequences wait for
-      // this round trip on every tile (4 chunks one by one 3.3 us of a tile's start)
-      constexpr int kBatch = VAR ? 4 : 1;
 #pragma unroll
-      for (int c0 = 0; c0 < kQtc; c0 += kBatch) {
-        uint32_t w[kBatch][32];
+      for (int c = 0; c < kQtc; ++c) {
+        uint32_t w[32];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-#pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            if (c0 + k >= kQtc) break;
-            const uint4 x = __ldg(qrow + 8 * (c0 + k) + g);
-            w[k][4 * g] = x.x;
-            w[k][4 * g + 1] = x.y;
-            w[k][4 * g + 2] = x.z;
-            w[k][4 * g + 3] = x.w;
-          }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-          if (c0 + k < kQtc) tmem_st32(tbase + lane_off + kQt + 32 * (c0 + k), w[k]);
+        for (int g = 0; g < 8; ++g) {
+          const uint4 x = __ldg(qrow + 8 * c + g);
+          w[4 * g] = x.x;
+          w[4 * g + 1] = x.y;
+          w[4 * g + 2] = x.z;
+          w[4 * g + 3] = x.w;
+        }
+        tmem_st32(tbase + lane_off + kQt + 32 * c, w);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -628,7 +668,67 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(p_ready_local + 8 * pb);  // release: P and the flag are visible first
       }
     }
-    if (ok) {
+    if constexpr (VAR) {
+      // ---------------------------------------------------------- epilogue, packed: O's rows through the P buffers
+      if (ok)
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait<false>(bar(bl.pv_done + (ntiles - 1) % kNpb), ((ntiles - 1) / kNpb) & 1, status));
+      if (ok && kNpb == 2 && ntiles >= 2)
+        ok = __all_sync(0xffffffffu, mbar_wait<false>(bar(bl.pv_done + (ntiles & 1)), ((ntiles - 2) >> 1) & 1, status));
+      tc_fence_after();
+      const float inv_l = l_sum > 0.f ? 1.f / l_sum : 0.f;
+#pragma unroll
+      for (int c = 0; c < kOCols / 32; ++c) {
+        // the O column of TMEM column 32 c of this lane, as below
+        int d0;
+        if constexpr (NC <= 8) {
+          d0 = (c < 4 || NC >= 7) ? 256 * (c >> 2) + 128 * kh + 32 * (c & 3) : 256 + 64 * kh + 32 * (c - 4);
+        } else if (c < 4) {
+          d0 = c < 2 * nv0 ? 64 * nv0 * kh + 32 * c : ow;
+        } else {
+          d0 = c - 4 < 2 * nv1 ? 256 + 64 * nv1 * kh + 32 * (c - 4) : ow;
+        }
+        uint32_t v[32];
+        tmem_ld32(tbase + lane_off + c * 32, v);
+        tmem_ld_wait();
+        if (d0 >= ow || !ok) continue;  // zero-filled V columns past D
+        const uint32_t at = p_sm + r * (2 * G::kOw);
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          st_shared_v4(at + (((d0 / 8 + g) ^ (r & 7)) << 4),
+                       pack2<BF16>(__uint_as_float(v[8 * g + 0]) * inv_l, __uint_as_float(v[8 * g + 1]) * inv_l),
+                       pack2<BF16>(__uint_as_float(v[8 * g + 2]) * inv_l, __uint_as_float(v[8 * g + 3]) * inv_l),
+                       pack2<BF16>(__uint_as_float(v[8 * g + 4]) * inv_l, __uint_as_float(v[8 * g + 5]) * inv_l),
+                       pack2<BF16>(__uint_as_float(v[8 * g + 6]) * inv_l, __uint_as_float(v[8 * g + 7]) * inv_l));
+      }
+      if (all_bar_and(3, ok)) {
+        typedef typename std::conditional<BF16, __nv_bfloat16, __half>::type T;
+        T* obase = reinterpret_cast<T*>(p.out) + b * p.o_sb + h * p.o_sh + o0;
+        // a warp's 16 rows, four at a time, whole rows per store
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int rr0 = 16 * (warp - 4) + 4 * k, orow = q0 + 64 * static_cast<int>(rank) + rr0;
+          uint4 x[4][2];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              ld_shared_v4(p_sm + (rr0 + i) * (2 * G::kOw) + (((lane + 32 * e) % (G::kOw / 8) ^ ((rr0 + i) & 7)) << 4),
+                           x[i][e].x, x[i][e].y, x[i][e].z, x[i][e].w);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (orow + i < p.Nq && lane + 32 * e < ow / 8)
+                *reinterpret_cast<uint4*>(obase + static_cast<int64_t>(orow + i) * p.o_sn + 8 * (lane + 32 * e)) = x[i][e];
+        }
+        if (kh == 0 && split == 0 && p.lse && row < p.Nq) {
+          constexpr float kLn2 = 0.6931471805599453f;
+          p.lse[(static_cast<int64_t>(b) * p.Hq + h) * stat_rows<VAR>(p) + row] =
+              l_sum > 0.f ? (m_used + __log2f(l_sum)) * kLn2 : -INFINITY;
+        }
+      }
+    } else if (ok) {
       // ---------------------------------------------------------- epilogue
       // the last P V of each buffer (their commits also arrive on the second
       // CTA); a key split may have no key tile at all
@@ -721,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (kh == 0 && split == 0 && p.lse && row < p.Nq) {
           constexpr float kLn2 = 0.6931471805599453f;
-          p.lse[(static_cast<int64_t>(b) * p.Hq + h) * stat_rows<VAR>(p) + row] =
+          p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.Nq + row] =
               l_sum > 0.f ? (m_used + __log2f(l_sum)) * kLn2 : -INFINITY;
         }
       }
@@ -745,10 +845,12 @@ cudaError_t launch_impl(const FwdParams& p_in, const FwdMaps& m, cudaStream_t st
   p.stages = kKSlots + Shape<NC>::kVSlots;
   p.slot_chunks = 2;
   // key splits and dropout are not combined (the host takes no key split with dropout)
-  auto kern = p.var.tiles ? fwd_fulld_kernel<NC, BF16, false, false, true>
-              : p.part_o  ? fwd_fulld_kernel<NC, BF16, true, false, false>
+  auto kern = p.part_o    ? fwd_fulld_kernel<NC, BF16, true, false, false>
               : p.dropout ? fwd_fulld_kernel<NC, BF16, false, true, false>
                           : fwd_fulld_kernel<NC, BF16, false, false, false>;
+  if constexpr (NC <= 10) {  // above, packed calls run in fwd_xch.cu
+    if (p.var.tiles) kern = fwd_fulld_kernel<NC, BF16, false, false, true>;
+  }
   constexpr int kNsplit = Shape<NC>::kNsplit;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
