@@ -56,19 +56,20 @@ __device__ __forceinline__ Pair block_scan(Pair v, Pair* total, Pair* sums) {
   return before;
 }
 
-// Slot of packed new token t, or -1 behind the last one or without a page.
-__device__ __forceinline__ int64_t token_slot(const PlanParams& p, int64_t t) {
-  if (t >= p.cu[p.B]) return -1;
+// Slot of packed new token t, or -1 behind the last one or without a page; the
+// requests' starts `cu` and lengths `lens` in shared memory or where they were written.
+__device__ __forceinline__ int64_t token_slot(const PlanParams& p, const int32_t* cu, const int32_t* lens, int64_t t) {
+  if (t >= cu[p.B]) return -1;
   int lo = 0, hi = p.B - 1;  // the last request that starts at or before t
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
-    if (p.cu[mid] <= t)
+    if (cu[mid] <= t)
       lo = mid;
     else
       hi = mid - 1;
   }
   // a request's first new token follows what it had: its length now less its new tokens
-  const int64_t pos = static_cast<int64_t>(p.lens_out[lo]) - (p.cu[lo + 1] - t);
+  const int64_t pos = static_cast<int64_t>(lens[lo]) - (cu[lo + 1] - t);
   const int64_t block = pos / p.page;
   if (block >= p.max_pages) return -1;
   const int page = p.table[lo * p.table_stride + block];
@@ -76,9 +77,11 @@ __device__ __forceinline__ int64_t token_slot(const PlanParams& p, int64_t t) {
 }
 
 // Lengths, starts and pages; with `slots_too` the slot map as well.
-__global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_constant__ PlanParams p, int slots_too) {
+__global__ void __launch_bounds__(kPlanThreads, 1) cache_plan_kernel(const __grid_constant__ PlanParams p, int slots_too) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ Pair sums[kPlanThreads / 32];
-  const int tid = threadIdx.x;
+  __shared__ int32_t s_cu[kPlanThreads + 1], s_lens[kPlanThreads];  // the last 1024 requests'
+  const int tid = threadIdx.x, lane = tid & 31;
   const int64_t head = *p.free_head;
   Pair carry = {0, 0};
   bool bad = head < 0 || head > p.n_free;
@@ -101,16 +104,29 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
     if (b < p.B) {
       p.cu[b] = static_cast<int32_t>(min(carry.a + at.a, static_cast<int64_t>(INT32_MAX)));
       p.lens_out[b] = len + add;
-      int32_t* row = p.table + b * p.table_stride;
-      for (int k = 0; k < need; ++k) {
-        if (had + k >= p.max_pages) {
+      s_cu[tid] = p.cu[b];
+      s_lens[tid] = len + add;
+    }
+    // a request's k-th new page; false without a page or a column for it
+    auto take = [&](int request, int col, int64_t f) {
+      if (col >= p.max_pages) return false;
+      const bool there = f >= 0 && f < p.n_free;
+      p.table[request * p.table_stride + col] = there ? p.free_pages[f] : -1;
+      return there;
+    };
+    const int64_t first = head + carry.b + at.b;
+    if (need > 0 && !take(b, had, first)) bad = true;
+    // prompts take many: the warp shares out the pages past a request's first
+    for (uint32_t todo = __ballot_sync(0xffffffffu, need > 1); todo; todo &= todo - 1) {
+      const int src = __ffs(todo) - 1;
+      const int n = __shfl_sync(0xffffffffu, need, src), col = __shfl_sync(0xffffffffu, had, src);
+      const int64_t f = __shfl_sync(0xffffffffu, first, src);
+      for (int k = 1 + lane; k < n; k += 32) {
+        if (col + k >= p.max_pages) {
           bad = true;
           break;
         }
-        const int64_t f = head + carry.b + at.b + k;
-        const bool there = f >= 0 && f < p.n_free;
-        row[had + k] = there ? p.free_pages[f] : -1;
-        bad |= !there;
+        if (!take(b - lane + src, col + k, f + k)) bad = true;
       }
     }
     carry.a += total.a;
@@ -118,18 +134,22 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
   }
   if (tid == 0) {
     p.cu[p.B] = static_cast<int32_t>(min(carry.a, static_cast<int64_t>(INT32_MAX)));
+    s_cu[min(p.B, kPlanThreads)] = p.cu[p.B];
     *p.free_head_out = static_cast<int32_t>(max(static_cast<int64_t>(0), min(head + carry.b, static_cast<int64_t>(p.n_free))));
     bad |= carry.a > p.max_new;
   }
   if (bad) record_error(p.status, FFPA_DEV_LENGTHS);
   if (!slots_too) return;
   __syncthreads();
-  for (int64_t t = tid; t < p.max_new; t += kPlanThreads) p.slots[t] = token_slot(p, t);
+  const bool here = p.B <= kPlanThreads;
+  for (int64_t t = tid; t < p.max_new; t += kPlanThreads)
+    p.slots[t] = here ? token_slot(p, s_cu, s_lens, t) : token_slot(p, p.cu, p.lens_out, t);
 }
 
 __global__ void __launch_bounds__(256) cache_slots_kernel(const __grid_constant__ PlanParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (t < p.max_new) p.slots[t] = token_slot(p, t);
+  if (t < p.max_new) p.slots[t] = token_slot(p, p.cu, p.lens_out, t);
 }
 
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __grid_constant__ AppendParams p) {
@@ -162,8 +182,14 @@ cudaError_t launch_cache_plan(const PlanParams& p, cudaStream_t s) {
   cache_plan_kernel<<<1, kPlanThreads, 0, s>>>(p, one ? 1 : 0);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || one) return e;
-  cache_slots_kernel<<<static_cast<unsigned>((p.max_new + 255) / 256), 256, 0, s>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.max_new + 255) / 256), 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  cfg.attrs = attr;
+  set_overlap(&attr[cfg.numAttrs++]);
+  return cudaLaunchKernelEx(&cfg, cache_slots_kernel, p);
 }
 
 cudaError_t launch_cache_append(const AppendParams& p, int sms, cudaStream_t s) {
