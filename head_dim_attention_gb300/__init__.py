@@ -26,6 +26,8 @@ from __future__ import annotations
 
 import math
 
+import torch
+
 from ._lib import (  # noqa: F401
     FfpaError,
     ffpa_bwd,
@@ -57,7 +59,6 @@ def attention_fwd(q, k, v, bias=None, causal=False, scale=None, out=None, lse=No
     dropout_p > 0 drops attention probabilities under the library's Philox
     contract (include/ffpa.h, ffpa_fwd_dropout) with the given seed and offset.
     """
-    import torch
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
     if out is None:
@@ -75,7 +76,6 @@ def attention_bwd(q, k, v, out, lse, dout, bias=None, causal=False, scale=None, 
                   stream=None, dropout_p=0.0, seed=0, offset=0):
     """dQ, dK, dV for the forward that produced ``out`` and ``lse`` (with the same
     dropout_p, seed and offset); allocates outputs if not given."""
-    import torch
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
     dq = torch.empty_like(q) if dq is None else dq
@@ -93,7 +93,6 @@ def attention_varlen_fwd(q, k, v, cu_seqlens, causal=False, scale=None, out=None
     token-major [T,H,D] tensor x is x.transpose(0, 1)[None]), sequence s in rows cu_seqlens[s] ..
     cu_seqlens[s+1]-1 (int32, on the device).  Rows outside the sequences are left as they are (unset where
     out/lse are allocated here)."""
-    import torch
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
     if out is None:
@@ -108,7 +107,6 @@ def attention_varlen_bwd(q, k, v, cu_seqlens, out, lse, dout, causal=False, scal
                          stream=None):
     """dQ, dK, dV of attention_varlen_fwd; allocates outputs if not given.  Rows outside the sequences are left
     as they are."""
-    import torch
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
     dq = torch.empty_like(q) if dq is None else dq
@@ -128,7 +126,6 @@ def attention_tree_fwd(q, k_cache, v_cache, block_table, seq_lens, draft_lens=No
     T, T]) marks, without one those up to itself.  T = 1 is plain decoding.
     Rows past a request's drafts are left as they are (unset where out/lse are
     allocated here)."""
-    import torch
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
     if out is None:
@@ -148,7 +145,6 @@ def cache_plan(lens, new_lens, block_table, free_pages, free_head, page_size, ma
     starts of the packed new tokens), slots (int64 [max_new], -1 behind the last
     one), lens_out and free_head_out; lens and free_head themselves may be
     given for the last two."""
-    import torch
     cu_new = lens.new_empty(lens.shape[0] + 1) if cu_new is None else cu_new
     slots = lens.new_empty(max_new, dtype=torch.int64) if slots is None else slots
     if slots.shape[0] != max_new:

@@ -224,13 +224,17 @@ def _pack_lse(t):
 
 
 def _ints(t, name, shape, dtype=torch.int32):
-    """Address of a contiguous integer (or bool) tensor of the given shape (-1: any size)."""
-    have = t.shape
-    if t.dtype is not dtype or len(have) != len(shape) or not t.is_contiguous() or \
-            any(w not in (-1, h) for w, h in zip(shape, have)):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} (-1: any size), got "
-                         f"{t.dtype} {tuple(have)}")
-    return t.data_ptr()
+    """Address of a contiguous integer (or bool) tensor of the given shape."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+                     f"{tuple(t.shape)}{'' if t.is_contiguous() else ', not contiguous'}")
+
+
+def _row(t, name, dtype=torch.int32):
+    """Address and size of a contiguous 1-D integer tensor."""
+    n = t.shape[0] if t.dim() == 1 else -1
+    return _ints(t, name, (n,), dtype), n
 
 
 def _device(*tensors) -> int:
@@ -249,9 +253,9 @@ def _raw_stream(stream, device):
 def ffpa_fwd_varlen(q, k, v, cu_seqlens, causal, scale, out, lse, stream=None) -> None:
     """Call ffpa_fwd_varlen (the forward over packed sequences); raises FfpaError on a non-zero status."""
     lib = load()
-    cu = _ints(cu_seqlens, "cu_seqlens", (-1,))
+    cu, n = _row(cu_seqlens, "cu_seqlens")
     dev = _device(q, k, v, cu_seqlens, out, lse)
-    rc = lib.ffpa_fwd_varlen(_pack(q), _pack(k), _pack(v), cu, cu_seqlens.shape[0] - 1, int(causal), scale, _pack(out),
+    rc = lib.ffpa_fwd_varlen(_pack(q), _pack(k), _pack(v), cu, n - 1, int(causal), scale, _pack(out),
                              _pack_lse(lse), _raw_stream(stream, dev))
     _raise(rc)
 
@@ -259,9 +263,9 @@ def ffpa_fwd_varlen(q, k, v, cu_seqlens, causal, scale, out, lse, stream=None) -
 def ffpa_bwd_varlen(q, k, v, cu_seqlens, causal, scale, out, lse, dout, dq, dk, dv, stream=None) -> None:
     """Call ffpa_bwd_varlen (the backward of ffpa_fwd_varlen); raises FfpaError on a non-zero status."""
     lib = load()
-    cu = _ints(cu_seqlens, "cu_seqlens", (-1,))
+    cu, n = _row(cu_seqlens, "cu_seqlens")
     dev = _device(q, k, v, cu_seqlens, out, lse, dout, dq, dk, dv)
-    rc = lib.ffpa_bwd_varlen(_pack(q), _pack(k), _pack(v), cu, cu_seqlens.shape[0] - 1, int(causal), scale, _pack(out),
+    rc = lib.ffpa_bwd_varlen(_pack(q), _pack(k), _pack(v), cu, n - 1, int(causal), scale, _pack(out),
                              _pack_lse(lse), _pack(dout), _pack(dq), _pack(dk), _pack(dv), _raw_stream(stream, dev))
     _raise(rc)
 
@@ -271,13 +275,14 @@ def ffpa_fwd_tree(q, k_cache, v_cache, block_table, seq_lens, draft_lens, tree_m
     """Call ffpa_fwd_tree (drafted tokens over a paged cache); raises FfpaError on a non-zero status."""
     lib = load()
     B, _, T, _ = q.shape
-    table, lens = _ints(block_table, "block_table", (B, -1)), _ints(seq_lens, "seq_lens", (B,))
+    pages = block_table.shape[-1]
+    table, lens = _ints(block_table, "block_table", (B, pages)), _ints(seq_lens, "seq_lens", (B,))
     drafts = None if draft_lens is None else _ints(draft_lens, "draft_lens", (B,))
-    mask = None if tree_mask is None else _ints(tree_mask, "tree_mask", (-1, T, T), torch.bool)
+    masks = 0 if tree_mask is None else tree_mask.shape[0]
+    mask = None if tree_mask is None else _ints(tree_mask, "tree_mask", (masks, T, T), torch.bool)
     dev = _device(q, k_cache, v_cache, block_table, seq_lens, draft_lens, tree_mask, out, lse)
-    rc = lib.ffpa_fwd_tree(_pack(q), _pack(k_cache), _pack(v_cache), table, block_table.shape[1], lens, drafts, mask,
-                           0 if tree_mask is None else tree_mask.shape[0], scale, _pack(out), _pack_lse(lse),
-                           _raw_stream(stream, dev))
+    rc = lib.ffpa_fwd_tree(_pack(q), _pack(k_cache), _pack(v_cache), table, pages, lens, drafts, mask, masks, scale,
+                           _pack(out), _pack_lse(lse), _raw_stream(stream, dev))
     _raise(rc)
 
 
@@ -285,14 +290,14 @@ def ffpa_cache_plan(lens, new_lens, page_size, block_table, free_pages, free_hea
                     free_head_out, stream=None) -> None:
     """Call ffpa_cache_plan (block tables and slots from request lengths); raises FfpaError on a non-zero status."""
     lib = load()
-    n = lens.shape[0]
+    (at_lens, n), (at_free, n_free), (at_slots, most) = _row(lens, "lens"), _row(free_pages, "free_pages"), \
+        _row(slots, "slots", torch.int64)
+    each, one, pages = (n,), (1,), block_table.shape[-1]
     dev = _device(lens, new_lens, block_table, free_pages, free_head, cu_new, slots, lens_out, free_head_out)
     rc = lib.ffpa_cache_plan(
-        _ints(lens, "lens", (n,)), _ints(new_lens, "new_lens", (n,)), n, page_size,
-        _ints(block_table, "block_table", (n, -1)), block_table.shape[1], _ints(free_pages, "free_pages", (-1,)),
-        free_pages.shape[0], _ints(free_head, "free_head", (1,)), _ints(cu_new, "cu_new", (n + 1,)),
-        _ints(slots, "slots", (-1,), torch.int64), slots.shape[0], _ints(lens_out, "lens_out", (n,)),
-        _ints(free_head_out, "free_head_out", (1,)), _raw_stream(stream, dev))
+        at_lens, _ints(new_lens, "new_lens", each), n, page_size, _ints(block_table, "block_table", (n, pages)), pages,
+        at_free, n_free, _ints(free_head, "free_head", one), _ints(cu_new, "cu_new", (n + 1,)), at_slots, most,
+        _ints(lens_out, "lens_out", each), _ints(free_head_out, "free_head_out", one), _raw_stream(stream, dev))
     _raise(rc)
 
 

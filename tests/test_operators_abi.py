@@ -75,13 +75,16 @@ def test_varlen_bwd_needs_everything(lib, name):
 
 
 def test_binding_checks_integer_tensors():
-    _lib._ints(torch.zeros(4, dtype=torch.int32), "cu_seqlens", (-1,))
-    _lib._ints(torch.zeros(2, 3, dtype=torch.int32), "block_table", (2, -1))
-    for bad in (torch.zeros(4, dtype=torch.int64), torch.zeros(2, 2, dtype=torch.int32), torch.zeros(8, dtype=torch.int32)[::2]):
+    assert _lib._row(torch.zeros(4, dtype=torch.int32), "cu_seqlens")[1] == 4
+    _lib._ints(torch.zeros(2, 3, dtype=torch.int32), "block_table", (2, 3))
+    for bad in (torch.zeros(4, dtype=torch.int64), torch.zeros(2, 2, dtype=torch.int32), torch.zeros(8, dtype=torch.int32)[::2],
+                torch.zeros((), dtype=torch.int32)):
         with pytest.raises(ValueError, match="cu_seqlens"):
-            _lib._ints(bad, "cu_seqlens", (-1,))
+            _lib._row(bad, "cu_seqlens")
     with pytest.raises(ValueError, match="seq_lens"):
         _lib._ints(torch.zeros(4, dtype=torch.int32), "seq_lens", (5,))
+    with pytest.raises(ValueError, match="block_table"):
+        _lib._ints(torch.zeros(3, dtype=torch.int32), "block_table", (3, 3))
 
 
 def test_packed_descriptors_are_the_described_ones():
