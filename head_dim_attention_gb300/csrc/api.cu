@@ -506,6 +506,16 @@ int bwd_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_tensor_t
   return cuda_rc(e != cudaSuccess ? e : e2);
 }
 
+// A first call on a device creates the scratch pool, looks up the status word and
+// loads kernels: none of it touches a stream, but a thread that captures one in
+// the default mode may not do it.  While this lives, it may, so a first call can
+// be a captured one.
+struct CaptureGuard {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  CaptureGuard() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~CaptureGuard() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
 // ------------------------------------------------------------ packed sequences
 // Checks beyond check_common: one batch, as many keys as queries, and the starts.
 int check_packed(const Common& c, const int32_t* cu_seqlens, int n_seqs, int causal) {
@@ -568,6 +578,7 @@ int fwd_varlen_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_t
   if ((rc = check_packed(c, cu_seqlens, n_seqs, causal))) return rc;
   if ((rc = check_bhnd(out, c.dtype, {c.B, c.Hq, c.Nq, c.D}))) return rc;
   if (lse && (rc = check_lse(lse, c))) return rc;
+  CaptureGuard guard;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint32_t* status = device_status_word();
   if (!status) return FFPA_ERR_CUDA;
@@ -607,6 +618,7 @@ int bwd_varlen_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_t
   if ((rc = check_bhnd(dv, c.dtype, {c.B, c.Hkv, c.Nkv, c.D}))) return rc;
   if (!lse) return FFPA_ERR_INVALID_ARG;
   if ((rc = check_lse(lse, c))) return rc;
+  CaptureGuard guard;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint32_t* status = device_status_word();
   if (!status) return FFPA_ERR_CUDA;
@@ -686,6 +698,7 @@ int fwd_tree_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* kc, const ffpa_te
     return rc;
   if (max_pages < 1 || (mask && mask_batch != 1 && mask_batch != c.B)) return FFPA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(max_pages) * kc->shape[2] > (1ll << 30)) return FFPA_ERR_UNSUPPORTED;
+  CaptureGuard guard;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint32_t* status = device_status_word();
   const int sms = device_sm_count();
@@ -759,6 +772,7 @@ int cache_plan_impl(const int32_t* lens, const int32_t* new_lens, int n_reqs, in
   p.max_pages = max_pages;
   p.n_free = n_free;
   p.max_new = max_new;
+  CaptureGuard guard;
   p.status = device_status_word();
   if (!p.status) return FFPA_ERR_CUDA;
   timing_begin();
@@ -793,6 +807,7 @@ int cache_append_impl(const ffpa_tensor_t* k, const ffpa_tensor_t* v, const ffpa
   p.D = (int)D;
   p.page = (int)kc->shape[2];
   p.n_pages = (int)kc->shape[0];
+  CaptureGuard guard;
   p.status = device_status_word();
   const int sms = device_sm_count();
   if (!p.status || sms <= 0) return FFPA_ERR_CUDA;

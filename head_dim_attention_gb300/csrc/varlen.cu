@@ -72,11 +72,24 @@ __global__ void __launch_bounds__(kPlanThreads) varlen_plan_kernel(const __grid_
     const int work = p.causal ? tile + 1 : tiles;
     return kBins - 1 - min(work >> p.bin_shift, kBins - 1);  // heaviest first
   };
-  for (int s = warp; s < p.n_seqs; s += kWarps) {
-    const SeqRange r = seq_range(p, s);
-    const int tiles = (r.len + kTileRows - 1) / kTileRows;
-    for (int t = lane; t < tiles; t += 32) atomicAdd(&count[bin(t, tiles)], 1);
-  }
+  // A warp takes 32 sequences at a time; a lane goes through the first tiles of its
+  // own (short sequences come by the thousand), the warp through the rest together.
+  auto each_tile = [&](auto&& visit) {
+    constexpr int kOwn = 4;
+    for (int s0 = 32 * warp; s0 < p.n_seqs; s0 += 32 * kWarps) {
+      const int s = s0 + lane;
+      const SeqRange r = s < p.n_seqs ? seq_range(p, s) : SeqRange{0, 0};
+      const int tiles = (r.len + kTileRows - 1) / kTileRows;
+      for (int t = 0; t < min(tiles, kOwn); ++t) visit(s, r, t, tiles);
+      for (uint32_t todo = __ballot_sync(0xffffffffu, tiles > kOwn); todo; todo &= todo - 1) {
+        const int src = __ffs(todo) - 1;
+        const SeqRange o = {__shfl_sync(0xffffffffu, r.start, src), __shfl_sync(0xffffffffu, r.len, src)};
+        const int n = __shfl_sync(0xffffffffu, tiles, src);
+        for (int t = kOwn + lane; t < n; t += 32) visit(s0 + src, o, t, n);
+      }
+    }
+  };
+  each_tile([&](int, const SeqRange&, int t, int tiles) { atomicAdd(&count[bin(t, tiles)], 1); });
   __syncthreads();
   // exclusive scan over the classes: each thread takes kBins / kPlanThreads of them
   constexpr int kPer = kBins / kPlanThreads;
@@ -103,15 +116,11 @@ __global__ void __launch_bounds__(kPlanThreads) varlen_plan_kernel(const __grid_
 #pragma unroll
   for (int i = 0; i < kPer; ++i) count[tid * kPer + i] = before + own[i];
   __syncthreads();
-  for (int s = warp; s < p.n_seqs; s += kWarps) {
-    const SeqRange r = seq_range(p, s);
-    const int tiles = (r.len + kTileRows - 1) / kTileRows;
-    for (int t = lane; t < tiles; t += 32) {
-      const int at = atomicAdd(&count[bin(t, tiles)], 1);
-      // overlapping ranges (starts that do not ascend) can have more tiles than slots
-      if (at < p.slots) p.tiles[at] = make_int4(s, t, r.start, r.len);
-    }
-  }
+  each_tile([&](int s, const SeqRange& r, int t, int tiles) {
+    const int at = atomicAdd(&count[bin(t, tiles)], 1);
+    // overlapping ranges (starts that do not ascend) can have more tiles than slots
+    if (at < p.slots) p.tiles[at] = make_int4(s, t, r.start, r.len);
+  });
   for (int i = all + tid; i < p.slots; i += kPlanThreads) p.tiles[i] = make_int4(-1, 0, 0, 0);
 }
 
