@@ -42,7 +42,7 @@ __device__ __forceinline__ void var_end() {
 }
 
 __device__ __forceinline__ VarTile var_tile(const VarParams& v, int slot) {
-  const int4 t = __ldg(v.tiles + slot);
+  const int4 t = __ldcg(v.tiles + slot);  // written by a launch that this one overlaps
   return VarTile{t.x, t.y, t.z, t.w};
 }
 
