@@ -117,12 +117,12 @@ struct Shape {
 
 struct Bars {
   int full_x, empty_x, full_g, empty_g, res_full, x_full, x_free, pt_full, pt_peer, pt_free, ds_full, ds_peer,
-      ds_free, st_ready, st_local, st_free, pm_ready, pm_local, drain_x, drain_g, g_done, count;
+      ds_free, st_ready, st_local, st_free, pm_ready, pm_local, drain_x, drain_g, g_done, st_full, count;
 };
 // rings: up to three slots; x_full, x_free, st_*: one per TMEM score buffer or
 // staging tile; pt_*, ds_*, pm_*: one per receive buffer (up to three)
 __host__ __device__ constexpr Bars bar_layout() {
-  return Bars{0, 3, 6, 9, 12, 13, 15, 17, 20, 23, 26, 29, 32, 35, 37, 39, 41, 44, 47, 48, 49, 50};
+  return Bars{0, 3, 6, 9, 12, 13, 15, 17, 20, 23, 26, 29, 32, 35, 37, 39, 41, 44, 47, 48, 49, 50, 51};
 }
 static_assert(bar_layout().count * 8 + 16 <= 512, "barrier area");
 
@@ -306,6 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(bl.drain_x), 1);
     mbar_init(bar(bl.drain_g), 1);
     mbar_init(bar(bl.g_done), 1);
+    mbar_init(bar(bl.st_full), 1);
     // the first use of each receive buffer: this CTA expects one tile's bytes
     for (int i = 0; i < kNrecv; ++i) mbar_expect_tx(bar((is_b ? bl.pt_full : bl.ds_full) + i), kTileX);
     fence_mbar_init();
@@ -339,7 +340,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 4; c < NC; ++c)
         tma_load_4d_pair(res_sm + (c - 4) * kHalf, mRes, lead(bl.res_full), c * kChunk, g.s_row0, g.hs, g.b);
     } else {
-      if constexpr (VAR) var_map_acquire(mG);
+      if constexpr (VAR) {
+        // the stationary tile's chunks 0..3 (this CTA's 64 rows) on their way to TMEM,
+        // through the staging tiles, idle until the first P or dS
+        static_assert(4 * kHalf <= kNstage * kTileX, "four chunks fit the staging tiles");
+        var_map_acquire(mRes);
+        mbar_expect_tx(bar(bl.st_full), 4 * kHalf);
+        for (int c = 0; c < 4; ++c)
+          tma_load_4d(stage_sm + c * kHalf, mRes, bar(bl.st_full), c * kChunk, g.s_row0, g.hs, g.b);
+        var_map_acquire(mG);
+      }
       tma_prefetch_desc(mG);
     }
     bool ok = true;
@@ -530,7 +540,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the other pair's CTA that holds the same rows receives this side's tiles
     const int o_full = is_b ? bl.ds_full : bl.pt_full;
     const int sfree = is_b ? bl.ds_free : bl.pt_free;  // this side's "the other's buffer is free"
-    {
+    if constexpr (VAR) {
+      // Read row by row from global memory (below), every load of a warp touches 32
+      // lines: 3 us at a tile's start, much of a short sequence's tile.
+      mbar_wait(bar(bl.st_full), 0, status);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t wv[32];
+#pragma unroll
+        for (int gq = 0; gq < 8; ++gq) {
+          const uint4 x = ld_shared_v4(swz(stage_sm + c * kHalf, r, gq));
+          wv[4 * gq] = x.x;
+          wv[4 * gq + 1] = x.y;
+          wv[4 * gq + 2] = x.z;
+          wv[4 * gq + 3] = x.w;
+        }
+        tmem_st32(tbase + lane_off + kSt + 32 * c, wv);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (pr == 0)
+          mbar_arrive(bar(bl.res_full));
+        else
+          mbar_arrive_remote(lead(bl.res_full));
+      }
+    } else {
       // chunks 0..3 of this thread's stationary row into its TMEM lane: 128
       // words of two 16-bit values in memory order, the TS form's A layout
       // (the threads of lanes r and r + 64 write the same row)
@@ -545,24 +581,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const uint4* srow_ptr = reinterpret_cast<const uint4*>(base + g.b * sb + g.hs * sh +
                                                              static_cast<int64_t>(min(srow, g.s_limit - 1)) * sn);
-      // kBatch chunks' loads are in flight together (packed sequences: this round
-      // trip is a large part of a short sequence's tile)
-      constexpr int kBatch = VAR ? 4 : 1;
 #pragma unroll
-      for (int c0 = 0; c0 < 4; c0 += kBatch) {
-        uint32_t wv[kBatch][32];
+      for (int c = 0; c < 4; ++c) {
+        uint32_t wv[32];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-#pragma unroll
-          for (int gq = 0; gq < 8; ++gq) {
-            const uint4 x = __ldg(srow_ptr + 8 * (c0 + k) + gq);
-            wv[k][4 * gq] = x.x;
-            wv[k][4 * gq + 1] = x.y;
-            wv[k][4 * gq + 2] = x.z;
-            wv[k][4 * gq + 3] = x.w;
-          }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) tmem_st32(tbase + lane_off + kSt + 32 * (c0 + k), wv[k]);
+        for (int gq = 0; gq < 8; ++gq) {
+          const uint4 x = __ldg(srow_ptr + 8 * c + gq);
+          wv[4 * gq] = x.x;
+          wv[4 * gq + 1] = x.y;
+          wv[4 * gq + 2] = x.z;
+          wv[4 * gq + 3] = x.w;
+        }
+        tmem_st32(tbase + lane_off + kSt + 32 * c, wv);
       }
       tmem_st_wait();
       tc_fence_before();
