@@ -739,7 +739,7 @@ int fwd_tree_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* kc, const ffpa_te
   if (scratch_alloc(&scratch, o_bytes + ml_bytes + p.blocks * sizeof(int4), st) != cudaSuccess) return FFPA_ERR_CUDA;
   p.part_o = static_cast<float*>(scratch);
   p.part_ml = reinterpret_cast<float*>(static_cast<char*>(scratch) + o_bytes);
-  p.starts = reinterpret_cast<int4*>(static_cast<char*>(scratch) + o_bytes + ml_bytes);
+  p.joins = reinterpret_cast<int4*>(static_cast<char*>(scratch) + o_bytes + ml_bytes);
   cudaError_t e = launch_fwd_tree(p, mk, mv, dtype_is_bf16(c.dtype), st);
   cudaError_t e2 = cudaFreeAsync(scratch, st);
   return cuda_rc(e != cudaSuccess ? e : e2);
@@ -984,4 +984,4 @@ extern "C" int ffpa_selftest_wait_timeout(ffpa_stream_t stream) {
   return cudaGetLastError() == cudaSuccess ? FFPA_OK : FFPA_ERR_CUDA;
 }
 
-extern "C" int ffpa_version(void) { return 100; }
+extern "C" int ffpa_version(void) { return 200; }

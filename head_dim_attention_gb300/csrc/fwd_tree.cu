@@ -9,7 +9,7 @@
 //
 // What bounds it: reading K and V once, 4 D bytes per key and kv head.  A tile
 // of 128 query rows would be mostly padding, so the operands are swapped: keys
-// and head-dimension columns are the MMA's M, the rows its N (16, 32, 64 or 96):
+// and head-dimension columns are the MMA's M, the rows its N (16, 32, 48, 64 or 96):
 //   S^T [128 keys, N]  = K_tile (K-major A) . Q^T (K-major B)
 //   O^T [128 columns, N] += V_tile^T (MN-major A) . P^T (K-major B)
 // O^T of all D columns stays in TMEM (ceil(D / 128) N columns of 512), the S^T
@@ -38,8 +38,8 @@
 //
 // Warps: 0 and 2 TMA producers (alternate ring slots; the lanes of a warp issue
 // a slot's boxes), 1 TMEM owner and MMA issuer, from 4 on softmax, correction
-// and epilogue: a warpgroup per 32 rows (thread = key of S^T, then column of
-// O^T).  Every wait is bounded.
+// and epilogue: a warpgroup per 32 rows, 16 at N = 16 and 48 (thread = key of S^T,
+// then column of O^T).  Every wait is bounded.
 #include <algorithm>
 #include <type_traits>
 
@@ -226,9 +226,6 @@ __device__ __forceinline__ void store1(void* base, int64_t at, float x) {
   else
     static_cast<__half*>(base)[at] = __float2half_rn(x);
 }
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
 __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
   asm volatile("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tst.shared.b16 [%0], h;\n\t}" ::"r"(addr), "r"(v) : "memory");
 }
@@ -298,9 +295,14 @@ __device__ __forceinline__ float reduce_columns(float (&v)[C], int lane, Op op) 
   return v[0];
 }
 
+// Rows of a softmax warpgroup, and the block's threads.
+template <int N>
+constexpr int tree_rows() {
+  return N == 16 || N == 48 ? 16 : 32;
+}
 template <int N>
 constexpr int tree_threads() {
-  return 128 + 128 * ((N + 31) / 32);
+  return 128 + 128 * (N / tree_rows<N>());
 }
 // Blocks per SM the registers allow for: two for N <= 32 (launched as two where
 // the shared memory of a small D allows it, see launch_n).
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(tree_threads<N>(), tree_residency<N>())
   typedef typename std::conditional<BF16, __nv_bfloat16, __half>::type T;
   constexpr int kThreads = tree_threads<N>();
   constexpr int kSoftWarps = kThreads / 32 - 4;
-  constexpr int C = N < 32 ? N : 32;       // rows per softmax thread
+  constexpr int C = tree_rows<N>();        // rows per softmax thread
   constexpr int kSBuf = N == 96 ? 1 : 2;   // S^T buffers: TMEM has room for one next to a 96-row O^T
   constexpr bool kLo = keeps_residual(N, BF16);
   constexpr Bars bl = bar_layout();
@@ -330,14 +332,15 @@ __global__ void __launch_bounds__(tree_threads<N>(), tree_residency<N>())
   uint64_t* bars = reinterpret_cast<uint64_t*>(misc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + bl.count);
   Walk<N>* start = reinterpret_cast<Walk<N>*>(misc + 176);  // the block's first segment (left == 0: none)
+  int* pieces = reinterpret_cast<int*>(misc + 252);         // of the unit that this block's start is the first inside
   int64_t* sums = reinterpret_cast<int64_t*>(misc + 256);
-  uint32_t* vis = reinterpret_cast<uint32_t*>(misc + 256 + 128);       // [3][128] draft -> rows that see it, 32 rows each
+  uint32_t* vis = reinterpret_cast<uint32_t*>(misc + 256 + 128);       // [3][128] draft -> rows that see it, C rows each
   int64_t* row_off = reinterpret_cast<int64_t*>(vis + 3 * 128);        // [N] offset of the row in out (0: padding)
   int64_t* row_lse = row_off + 96;                                     // [N] index of the row in lse
   float* stat = reinterpret_cast<float*>(row_lse + 96);                // [warps][32] exchanged statistics
   float* bcast = stat + 12 * 32;                                       // [warps][32] per-row values of one warp
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
-  static_assert(bl.count * 8 + 4 <= 176 && 176 + sizeof(Walk<N>) <= 256, "barrier area");
+  static_assert(bl.count * 8 + 4 <= 176 && 176 + sizeof(Walk<N>) <= 252, "barrier area");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t* status = p.status;
@@ -357,6 +360,7 @@ __global__ void __launch_bounds__(tree_threads<N>(), tree_residency<N>())
     mbar_init(bar(bl.drain), 1);
     fence_mbar_init();
     start->left = 0;
+    *pieces = 0;
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), p.tmem_cols);
@@ -385,14 +389,19 @@ __global__ void __launch_bounds__(tree_threads<N>(), tree_residency<N>())
           Walk<N> first;
           first.begin(p, b, r, w0 - at, w1 - w0);
           *start = first;
+          // For the merge kernel: a unit that begins in the block before and goes on in
+          // this one is joined from here; its pieces are that block's and those of the
+          // blocks that start inside it, w_c < unit_end <=> c < unit_end blocks / total.
+          if (first.tile > 0 && first.tile <= w0 - block_start(w.total, blocks, c - 1)) {
+            const int64_t unit_end = w0 - first.tile + first.tiles;
+            *pieces = static_cast<int>((unit_end * blocks + w.total - 1) / w.total) - c + 1;
+          }
         }
       }
     }
   }
   __syncthreads();
-  // where this block starts, for the merge kernel
-  if (tid == 0)
-    p.starts[blockIdx.x] = start->left > 0 ? make_int4(start->b, start->sub, start->tile, start->r.m) : make_int4(-1, 0, 0, 0);
+  if (tid == 0) p.joins[blockIdx.x] = make_int4(*pieces, start->b, start->sub, start->r.m);
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
   const bool any = start->left > 0;
@@ -587,12 +596,12 @@ __global__ void __launch_bounds__(tree_threads<N>(), tree_residency<N>())
         row_lse[st] = li;
       }
       if (w.end * kTileRows > prefix) {  // this segment has drafts among its keys
-        // item (draft j, 32 rows g): a bit for each row that sees the draft
-        for (int it = st; it < ((N + 31) / 32) * m; it += kAll) {
+        // item (draft j, C rows g): a bit for each row that sees the draft
+        for (int it = st; it < (N / C) * m; it += kAll) {
           const int j = it % m, g = it / m;
           uint32_t bits = 0;
           for (int x = 0; x < C; ++x) {
-            const int rr = w.row0 + g * 32 + x;
+            const int rr = w.row0 + g * C + x;
             if (rr >= rows) break;
             const int i = rr % m;
             const bool see = p.mask ? __ldg(p.mask + w.b * p.mask_sb + static_cast<int64_t>(i) * p.T + j) != 0 : j <= i;
@@ -778,39 +787,26 @@ __global__ void __launch_bounds__(tree_threads<N>(), tree_residency<N>())
   }
 }
 
-// Joins the partials of the units that cross blocks.  Block (c, y) looks at the
-// place where attention block c starts: if that is inside a unit, and the
-// first such place in it, its warps merge rows 4 y .. of the unit, one each.  The
-// unit's first piece is slot 1 of block c - 1, the others slot 0 of the blocks
-// from c on.
+// Joins the partials of the units that cross blocks.  Such a unit begins in a
+// block c - 1 (its slot 1) and goes on in the blocks from c on (their slots 0);
+// attention block c leaves its place and number of pieces in joins[c].  A warp takes
+// Q x 128 columns of a row:
 //   O = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c
-// Latency bounds it (three dependent reads and, per 32 pieces, one round of
-// loads), so many small blocks: a warp per row, Q = ceil(D / 128) to a power of
-// two float4 of it per lane.
+// This form is for many units, each of few pieces.  Latency bounds it: the place,
+// the maxima and sums, then 16 / Q partial rows in flight at a time.
 template <int N, bool BF16, int Q>
-__global__ void __launch_bounds__(kMergeThreads, Q == 8 ? 5 : 8) tree_merge_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int x = blockIdx.y * (kMergeThreads / 32) + warp;
-  const int4 prev = p.starts[c - 1], at = p.starts[c];
-  // the starts that follow, 32 at a time: how many more are inside the unit
-  int4 next = make_int4(-1, 0, 0, 0);
-  if (c + 1 + lane < p.blocks) next = p.starts[c + 1 + lane];
-  if (at.x < 0 || at.z == 0) return;                           // idle, or at a unit's start
-  if (prev.x == at.x && prev.y == at.y && prev.z > 0) return;  // not the first
-  const int b = at.x, sub = at.y, m = at.w;
+  constexpr int kDeep = 16 / Q;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x + 1;
+  const int4 join = p.joins[c];
+  const int pieces = join.x, b = join.y, sub = join.z, m = join.w;
+  if (pieces == 0) return;
+  const int parts = (p.D + 128 * Q - 1) / (128 * Q);  // warps of a row
+  const int item = blockIdx.y * (kMergeThreads / 32) + warp, x = item / parts, d0 = 128 * Q * (item % parts) + 4 * lane;
   const int rt = (p.group * m + N - 1) / N;
   const int rr = (sub % rt) * N + x;
   if (x >= N || rr >= p.group * m) return;
-  int pieces = 2;
-  for (int k = c + 1;;) {
-    const uint32_t in = __ballot_sync(0xffffffffu, next.x == b && next.y == sub && next.z > 0);
-    const int run = __ffs(~in) - 1;
-    pieces += run < 0 ? 32 : run;
-    if (run >= 0) break;
-    k += 32;
-    next = k + lane < p.blocks ? p.starts[k + lane] : make_int4(-1, 0, 0, 0);
-  }
   auto slot = [&](int k) { return (2 * static_cast<int64_t>(c - 1 + k) + (k == 0 ? 1 : 0)) * N + x; };
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
   float M = -INFINITY;
@@ -819,7 +815,7 @@ __global__ void __launch_bounds__(kMergeThreads, Q == 8 ? 5 : 8) tree_merge_kern
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   const float ref = M == -INFINITY ? 0.f : M;
   float sum = 0.f;
-  float4 o[Q];  // columns 4 lane + 128 q ..
+  float4 o[Q];  // columns d0 + 128 q ..
 #pragma unroll
   for (int q = 0; q < Q; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int k0 = 0; k0 < pieces; k0 += 32) {
@@ -830,31 +826,37 @@ __global__ void __launch_bounds__(kMergeThreads, Q == 8 ? 5 : 8) tree_merge_kern
       sum = fmaf(f, s.y, sum);
     }
     const int n = min(32, pieces - k0);
-#pragma unroll(Q >= 4 ? 2 : 4)
-    for (int k = 0; k < n; ++k) {
-      const float fk = __shfl_sync(0xffffffffu, f, k);
-      const float4* src = reinterpret_cast<const float4*>(p.part_o + slot(k0 + k) * p.D) + lane;
+    for (int k1 = 0; k1 < n; k1 += kDeep) {
+      float4 y[kDeep][Q];
 #pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        if (4 * lane + 128 * q < p.D) {
-          const float4 y = src[32 * q];
-          o[q].x = fmaf(fk, y.x, o[q].x);
-          o[q].y = fmaf(fk, y.y, o[q].y);
-          o[q].z = fmaf(fk, y.z, o[q].z);
-          o[q].w = fmaf(fk, y.w, o[q].w);
+      for (int k = 0; k < kDeep; ++k)
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+          y[k][q] = *reinterpret_cast<const float4*>(p.part_o + slot(min(k0 + k1 + k, pieces - 1)) * p.D +
+                                                     min(d0 + 128 * q, p.D - 4));
+#pragma unroll
+      for (int k = 0; k < kDeep; ++k) {
+        if (k1 + k >= n) break;
+        const float fk = __shfl_sync(0xffffffffu, f, (k1 + k) & 31);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          o[q].x = fmaf(fk, y[k][q].x, o[q].x);
+          o[q].y = fmaf(fk, y[k][q].y, o[q].y);
+          o[q].z = fmaf(fk, y[k][q].z, o[q].z);
+          o[q].w = fmaf(fk, y[k][q].w, o[q].w);
         }
       }
     }
   }
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  for (int e = 16; e > 0; e >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, e);
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   const int h = (sub / rt) * p.group + rr / m, i = rr % m;
   typedef typename std::conditional<BF16, __nv_bfloat16, __half>::type T;
   T* orow = static_cast<T*>(p.out) + b * p.o_sb + h * p.o_sh + i * p.o_sn;
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
-    const int d = 4 * lane + 128 * q;
+    const int d = d0 + 128 * q;
     if (d < p.D) {
       uint2 w;
       w.x = pack2<BF16>(o[q].x * inv, o[q].y * inv);
@@ -863,26 +865,147 @@ __global__ void __launch_bounds__(kMergeThreads, Q == 8 ? 5 : 8) tree_merge_kern
     }
   }
   constexpr float kLn2 = 0.6931471805599453f;
-  if (lane == 0 && p.lse)
+  if (d0 == 0 && p.lse)
     p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.T + i] = sum > 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
 }
 
+// The form for few units of many pieces (one long request: up to a piece per block).
+// Block (u, y) takes 128 columns of a row of the u-th unit to join; its warps share
+// out the pieces, eight partial rows in flight each, and add up in shared memory.
+constexpr int kDeepThreads = 512;
 template <int N, bool BF16>
-cudaError_t launch_merge(const TreeParams& p, cudaStream_t st) {
+__global__ void __launch_bounds__(kDeepThreads) tree_merge_deep_kernel(const __grid_constant__ TreeParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int kWarps = kDeepThreads / 32, kDeep = 8;
+  __shared__ int found[kWarps];
+  __shared__ int4 place;
+  __shared__ int first;
+  __shared__ float weight[kDeepThreads];
+  __shared__ float part_max[kWarps], part_sum[kWarps];
+  __shared__ float4 acc[kWarps][32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the u-th block with pieces to join (at most kDeepThreads blocks, see launch_merge)
+  int4 join = make_int4(0, 0, 0, 0);
+  if (tid < p.blocks) join = p.joins[tid];
+  const uint32_t have = __ballot_sync(0xffffffffu, join.x > 0);
+  if (lane == 0) found[warp] = __popc(have);
+  if (tid == 0) place = make_int4(0, 0, 0, 0);
+  __syncthreads();
+  int before = __popc(have & ((1u << lane) - 1u));
+  for (int w = 0; w < warp; ++w) before += found[w];
+  if (join.x > 0 && before == static_cast<int>(blockIdx.x)) {
+    place = join;
+    first = tid;
+  }
+  __syncthreads();
+  const int pieces = place.x, b = place.y, sub = place.z, m = place.w;
+  if (pieces == 0) return;
+  const int c = first, parts = (p.D + 127) / 128;
+  const int x = blockIdx.y / parts, d = 128 * (blockIdx.y % parts) + 4 * lane;
+  const int rt = (p.group * m + N - 1) / N;
+  const int rr = (sub % rt) * N + x;
+  if (rr >= p.group * m) return;
+  auto slot = [&](int k) { return (2 * static_cast<int64_t>(c - 1 + k) + (k == 0 ? 1 : 0)) * N + x; };
+  // a piece per thread: the maximum, the weights and the sum
+  const float2 s = tid < pieces ? reinterpret_cast<const float2*>(p.part_ml)[slot(tid)] : make_float2(-INFINITY, 0.f);
+  float M = s.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) part_max[warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, part_max[w]);
+  const float f = ex2(s.x - (M == -INFINITY ? 0.f : M));
+  weight[tid] = f;
+  float sum = f * s.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) part_sum[warp] = sum;
+  __syncthreads();
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float* src = p.part_o + min(d, p.D - 4);
+  for (int k0 = warp; k0 < pieces; k0 += kDeep * kWarps) {
+    float4 y[kDeep];
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i)
+      y[i] = *reinterpret_cast<const float4*>(src + slot(min(k0 + i * kWarps, pieces - 1)) * p.D);
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) {
+      if (k0 + i * kWarps >= pieces) break;
+      const float w = weight[k0 + i * kWarps];
+      o.x = fmaf(w, y[i].x, o.x);
+      o.y = fmaf(w, y[i].y, o.y);
+      o.z = fmaf(w, y[i].z, o.z);
+      o.w = fmaf(w, y[i].w, o.w);
+    }
+  }
+  acc[warp][lane] = o;
+  __syncthreads();
+  if (warp > 0) return;
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) sum += part_sum[w];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) {
+    const float4 y = acc[w][lane];
+    o.x += y.x;
+    o.y += y.y;
+    o.z += y.z;
+    o.w += y.w;
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const int h = (sub / rt) * p.group + rr / m, i = rr % m;
+  if (d < p.D) {
+    typedef typename std::conditional<BF16, __nv_bfloat16, __half>::type T;
+    uint2 w;
+    w.x = pack2<BF16>(o.x * inv, o.y * inv);
+    w.y = pack2<BF16>(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + b * p.o_sb + h * p.o_sh + i * p.o_sn + d) = w;
+  }
+  constexpr float kLn2 = 0.6931471805599453f;
+  if (d == 0 && p.lse)
+    p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.T + i] = sum > 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
+}
+
+template <int N, bool BF16, int Q>
+cudaError_t launch_merge_q(const TreeParams& p, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  const int most = std::min(N, p.group * p.T);  // rows of a row tile, at most
-  cfg.gridDim = dim3(p.blocks - 1, (most + kMergeThreads / 32 - 1) / (kMergeThreads / 32), 1);
+  const int rows = std::min(N, p.group * p.T);  // of a row tile, at most
+  const int warps = rows * ((p.D + 128 * Q - 1) / (128 * Q)), per = kMergeThreads / 32;
+  cfg.gridDim = dim3(p.blocks - 1, (warps + per - 1) / per, 1);
   cfg.blockDim = dim3(kMergeThreads, 1, 1);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  set_overlap(&attr[0]);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (p.D <= 128) return cudaLaunchKernelEx(&cfg, tree_merge_kernel<N, BF16, 1>, p);
-  if (p.D <= 256) return cudaLaunchKernelEx(&cfg, tree_merge_kernel<N, BF16, 2>, p);
-  if (p.D <= 512) return cudaLaunchKernelEx(&cfg, tree_merge_kernel<N, BF16, 4>, p);
-  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<N, BF16, 8>, p);
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<N, BF16, Q>, p);
+}
+
+// Few units (fewer than a quarter of the blocks: five pieces or more on average)
+// take the deep form, as long as its blocks are two waves or so.  One request of
+// 131,072 keys, 8 heads on one kv head, D = 512 (152 pieces): 88 us in the wide form,
+// 58 in the deep one; 12 requests of 96 rows on two kv heads (19 pieces, 9216 deep
+// blocks): 126 and 155.
+template <int N, bool BF16>
+cudaError_t launch_merge(const TreeParams& p, cudaStream_t st) {
+  const int64_t units = static_cast<int64_t>(p.B) * p.Hkv * ((static_cast<int64_t>(p.group) * p.T + N - 1) / N);
+  const int items = std::min(N, p.group * p.T) * ((p.D + 127) / 128);  // of a unit: 128 columns of a row
+  if (units * 4 < p.blocks && units * items <= 8 * p.blocks && p.blocks <= kDeepThreads) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(units, p.blocks - 1)), items, 1);
+    cfg.blockDim = dim3(kDeepThreads, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    set_overlap(&attr[0]);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_merge_deep_kernel<N, BF16>, p);
+  }
+  if (p.D <= 128) return launch_merge_q<N, BF16, 1>(p, st);
+  if (p.D <= 256) return launch_merge_q<N, BF16, 2>(p, st);
+  if (p.D <= 512) return launch_merge_q<N, BF16, 4>(p, st);
+  return launch_merge_q<N, BF16, 8>(p, st);
 }
 
 template <int N, bool BF16>
@@ -905,6 +1028,7 @@ cudaError_t launch_tree(const TreeParams& p, const CUtensorMap& mk, const CUtens
   switch (p.rows_n) {
     case 16: return launch_n<16, BF16>(p, mk, mv, st);
     case 32: return launch_n<32, BF16>(p, mk, mv, st);
+    case 48: return launch_n<48, BF16>(p, mk, mv, st);
     case 64: return launch_n<64, BF16>(p, mk, mv, st);
     default: return launch_n<96, BF16>(p, mk, mv, st);
   }
@@ -916,16 +1040,16 @@ cudaError_t launch_tree(const TreeParams& p, const CUtensorMap& mk, const CUtens
 //
 // Rows: the fewest row tiles (each reads K and V again), then the smallest N.
 // O^T takes ceil(D / 128) N columns of TMEM next to the scores, Q and P 2 N D +
-// 1024 N bytes of shared memory next to the ring, so N = 96 serves D <= 512 and
-// N = 64 D <= 768.
+// 512 N (1024 N with the residual) bytes of shared memory next to the ring, so
+// N = 96 serves D <= 512, N = 64 D <= 768 and N = 48 D <= 1024.
 //
 // Two blocks per SM for D <= 256 and N <= 32, where a tile's chain (scores,
 // softmax, product) takes longer than its bytes.
 int tree_shape(TreeParams* p, int64_t rows, bool bf16) {
-  const int widest = p->D <= 512 ? 96 : p->D <= 768 ? 64 : 32;
+  const int widest = p->D <= 512 ? 96 : p->D <= 768 ? 64 : 48;
   const int64_t tiles = (rows + widest - 1) / widest;
   int n = widest;
-  for (int c : {64, 32, 16})
+  for (int c : {64, 48, 32, 16})
     if (c < widest && (rows + c - 1) / c == tiles) n = c;
   p->rows_n = n;
   p->slot_bytes = std::min(2, p->n_chunks) * kChunkBytes;

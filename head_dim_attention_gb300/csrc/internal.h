@@ -127,7 +127,8 @@ struct TreeParams {
   int blocks;                 // blocks of the attention kernel
   float* part_o;              // [2 blocks, rows_n, D] fp32 partials
   float* part_ml;             // [2 blocks, rows_n, 2] their (max, sum), log2 domain
-  int4* starts;               // [blocks] (request or -1, kv head x row tiles + row tile, key tile, drafts)
+  int4* joins;                // [blocks] (pieces to join from this block on, or 0; request, kv head x row tiles +
+                              // row tile, drafts)
   uint32_t* status;
 };
 // Sets rows_n, the ring and the TMEM columns; returns the blocks per SM.

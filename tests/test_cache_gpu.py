@@ -174,7 +174,9 @@ def test_one_token(lens, T, Hq, Hkv, D, page, dtype):
     ([260, 199], [33, 20], 33, 2, 1, 1024, 16, BF, "tree"),          # 66 rows of 32
     ([900], [128], 128, 4, 4, 256, 256, FP, "tree"),
     ([150, 40], [16, 9], 16, 4, 2, 768, 32, BF, None),
-    ([333, 90], [12, 12], 12, 4, 1, 448, 16, BF, "tree"),            # 48 rows of 64
+    ([333, 90], [12, 12], 12, 4, 1, 448, 16, BF, "tree"),            # 48 rows
+    ([300, 64, 130], [20, 5, 11], 20, 4, 2, 896, 32, BF, "tree"),    # 40 rows of 48
+    ([200, 140], [33, 25], 33, 4, 2, 1024, 64, FP, None),            # 66 rows of 48
 ])
 def test_drafts(lens, drafts, T, Hq, Hkv, D, page, dtype, mask):
     run_tree(lens, drafts, T, Hq, Hkv, D, page, dtype, mask=mask, seed=1)
@@ -183,6 +185,8 @@ def test_drafts(lens, drafts, T, Hq, Hkv, D, page, dtype, mask):
 def test_long_context_is_shared_out_and_joined():
     run_tree([9000, 1, 4100], [4, 1, 2], 4, 4, 2, 512, 64, BF, mask="tree", seed=2)
     run_tree([20000], [1], 1, 1, 1, 64, 16, FP, seed=3)
+    run_tree([9999], [3], 3, 8, 1, 512, 64, BF, mask="tree", seed=4)   # many pieces of one unit
+    run_tree([5000, 7], [11, 7], 11, 2, 1, 1024, 16, FP, seed=5)
 
 
 def test_many_requests():
