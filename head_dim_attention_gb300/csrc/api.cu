@@ -96,13 +96,14 @@ void tma_strides(const ffpa_tensor_t* t, int64_t out[3]) {
   out[2] = sb;
 }
 
-int encode_map(CUtensorMap* m, const ffpa_tensor_t* t, int box_rows = kTileRows) {
+// The map of the tensor's first `rows` rows (0: all of them).
+int encode_map(CUtensorMap* m, const ffpa_tensor_t* t, int box_rows = kTileRows, int64_t rows = 0) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return FFPA_ERR_CUDA;
   int64_t st[3];
   tma_strides(t, st);
-  const cuuint64_t dims[4] = {(cuuint64_t)t->shape[3], (cuuint64_t)t->shape[2], (cuuint64_t)t->shape[1],
-                              (cuuint64_t)t->shape[0]};
+  const cuuint64_t dims[4] = {(cuuint64_t)t->shape[3], (cuuint64_t)(rows ? rows : t->shape[2]),
+                              (cuuint64_t)t->shape[1], (cuuint64_t)t->shape[0]};
   const cuuint64_t strides[3] = {(cuuint64_t)st[0] * 2, (cuuint64_t)st[1] * 2, (cuuint64_t)st[2] * 2};
   const cuuint32_t box[4] = {(cuuint32_t)kChunk, (cuuint32_t)box_rows, 1, 1};
   const cuuint32_t es[4] = {1, 1, 1, 1};
@@ -548,7 +549,6 @@ void fill_plan(VarPlan* plan, VarParams* var, const VarLayout& l, const Common& 
   var->tiles = reinterpret_cast<const int4*>(scratch + l.maps_bytes);
   var->slots = l.slots;
   var->total = static_cast<int>(c.Nq);
-  plan->n_maps = 0;
   plan->cu = cu;
   plan->n_seqs = n_seqs;
   plan->total = static_cast<int>(c.Nq);
@@ -561,12 +561,16 @@ void fill_plan(VarPlan* plan, VarParams* var, const VarLayout& l, const Common& 
   plan->status = status;
 }
 
-void plan_map(VarPlan* plan, const CUtensorMap& m, const ffpa_tensor_t* t) {
+// Adds map `m` of `t` (box_rows rows to a box) to the plan.
+int plan_map(VarPlan* plan, const CUtensorMap& m, const ffpa_tensor_t* t, int box_rows) {
   int64_t st[3];
   tma_strides(t, st);
-  plan->maps[plan->n_maps] = m;
-  plan->base[plan->n_maps] = t->data;
-  plan->row_stride[plan->n_maps++] = st[0];
+  const int i = plan->n_maps++;
+  plan->maps[i] = plan->short_maps[i] = m;
+  plan->base[i] = t->data;
+  plan->row_stride[i] = st[0];
+  plan->short_rows[i] = varlen_short_rows(t->shape[3], t->shape[2], t->shape[1], st[0], st[1]);
+  return plan->short_rows[i] ? encode_map(&plan->short_maps[i], t, box_rows, 1) : FFPA_OK;
 }
 
 int fwd_varlen_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_tensor_t* v, const int32_t* cu_seqlens,
@@ -586,16 +590,18 @@ int fwd_varlen_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_t
   fill_fwd(&p, c, q, nullptr, causal, scale, out, lse, status);
   FwdMaps m;
   if ((rc = encode_fwd_maps(&m, q, k, v))) return rc;
+  VarPlan plan;
+  plan.n_maps = 0;
+  const bool pair = c.D >= 320;  // the CTA-pair kernels load halves of the Q and K tiles
+  const int half = pair ? kTileRows / 2 : kTileRows;
+  if ((rc = plan_map(&plan, pair ? m.q_half : m.q, q, half)) || (rc = plan_map(&plan, pair ? m.k_half : m.k, k, half)) ||
+      (rc = plan_map(&plan, m.v, v, kTileRows)))
+    return rc;
   const VarLayout l = var_layout(c.Nq, n_seqs);
   timing_begin();
   void* scratch = nullptr;
   if (scratch_alloc(&scratch, l.bytes, st) != cudaSuccess) return FFPA_ERR_CUDA;
-  VarPlan plan;
   fill_plan(&plan, &p.var, l, c, cu_seqlens, n_seqs, causal, static_cast<char*>(scratch), status);
-  const bool pair = c.D >= 320;  // the CTA-pair kernels load halves of the Q and K tiles
-  plan_map(&plan, pair ? m.q_half : m.q, q);
-  plan_map(&plan, pair ? m.k_half : m.k, k);
-  plan_map(&plan, m.v, v);
   timing_mark(st);
   cudaError_t e = launch_varlen_plan(plan, st);
   if (e == cudaSuccess) e = launch_fwd_main(p, m, dtype_is_bf16(c.dtype), st);
@@ -626,6 +632,15 @@ int bwd_varlen_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_t
   fill_bwd(&p, c, q, k, v, nullptr, causal, scale, out, lse, dout, dq, dk, dv, status);
   BwdMaps m;
   if ((rc = encode_bwd_maps(&m, q, k, v, dout))) return rc;
+  VarPlan plan;
+  plan.n_maps = 0;
+  const bool pair = c.D >= 320;
+  const int half = pair ? kTileRows / 2 : kTileRows;
+  if ((rc = plan_map(&plan, pair ? m.q_half : m.q, q, half)) || (rc = plan_map(&plan, pair ? m.k_half : m.k, k, half)) ||
+      (rc = plan_map(&plan, pair ? m.v_half : m.v, v, half)) ||
+      (rc = plan_map(&plan, pair ? m.dout_half : m.dout, dout, half)) ||
+      (pair && (rc = plan_map(&plan, m.k, k, kTileRows))))
+    return rc;
   const VarLayout l = var_layout(c.Nq, n_seqs);
   const size_t rows = static_cast<size_t>(c.Hq) * c.Nq;
   timing_begin();
@@ -633,20 +648,7 @@ int bwd_varlen_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_t
   if (scratch_alloc(&scratch, l.bytes + rows * 2 * sizeof(float), st) != cudaSuccess) return FFPA_ERR_CUDA;
   p.delta = reinterpret_cast<float*>(static_cast<char*>(scratch) + l.bytes);
   p.lse2 = p.delta + rows;
-  VarPlan plan;
   fill_plan(&plan, &p.var, l, c, cu_seqlens, n_seqs, causal, static_cast<char*>(scratch), status);
-  if (c.D >= 320) {
-    plan_map(&plan, m.q_half, q);
-    plan_map(&plan, m.k_half, k);
-    plan_map(&plan, m.v_half, v);
-    plan_map(&plan, m.dout_half, dout);
-    plan_map(&plan, m.k, k);
-  } else {
-    plan_map(&plan, m.q, q);
-    plan_map(&plan, m.k, k);
-    plan_map(&plan, m.v, v);
-    plan_map(&plan, m.dout, dout);
-  }
   timing_mark(st);
   cudaError_t e = launch_varlen_plan(plan, st);
   if (e == cudaSuccess) e = launch_bwd(p, m, dtype_is_bf16(c.dtype), st);

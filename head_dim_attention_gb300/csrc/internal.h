@@ -28,9 +28,11 @@ struct VarParams {
   int total;                // rows of q, k and v: the head stride of lse, delta and lse2
 };
 struct VarPlan {
-  CUtensorMap maps[kVarMaps];    // of the whole packed tensors
+  CUtensorMap maps[kVarMaps];        // of the whole packed tensors
+  CUtensorMap short_maps[kVarMaps];  // of their first rows: sequences of at most short_rows start from these
   const void* base[kVarMaps];    // their data pointers
   int64_t row_stride[kVarMaps];  // elements
+  int short_rows[kVarMaps];
   int n_maps;
   const int32_t* cu;             // [n_seqs + 1] first rows, ascending
   int n_seqs, total, slots, causal;
@@ -221,6 +223,8 @@ inline void set_overlap(cudaLaunchAttribute* attr) {
 }
 // Fills the tile slots and the per-sequence maps of a packed call (varlen.cu).
 cudaError_t launch_varlen_plan(const VarPlan& p, cudaStream_t s);
+// Rows of the longest sequence whose maps are made from short_maps (0: none); row and head strides in elements.
+int varlen_short_rows(int64_t D, int64_t rows, int64_t heads, int64_t row_stride, int64_t head_stride);
 
 cudaError_t launch_fwd_main(const FwdParams& p, const FwdMaps& m, bool bf16, cudaStream_t s);
 // Full-D CTA-pair forward (fwd_fulld.cu): D = 512, one pair holds all of O.

@@ -223,3 +223,23 @@ def test_gradient_against_differences():
         along = float((grads[i].double() * d).sum())
         room = 4 * HALF_STEP[FP] * float((grads[i].double().abs() * d.abs()).sum())
         assert abs(slope - along) <= room
+
+
+@pytest.mark.parametrize("D", range(64, 1025, 64))
+def test_small_tensors(D):
+    """Head dimensions and head counts of every kernel, over tensors and sequences that span a few KB to a few MB."""
+    pick = [0, 1, 2, 17, 63, 64, 65, 100, 127, 128, 129, 200, 255, 256, 257, 390]
+    host = torch.Generator().manual_seed(D)
+    draw = lambda n: int(torch.randint(n, (1,), generator=host))  # noqa: E731
+    for case in range(6):
+        Hkv = 1 + draw(3)
+        Hq, dtype, causal, token_major = Hkv * (1, 2, 4, 5)[draw(4)], (BF, FP)[case % 2], draw(3) > 0, draw(2) == 1
+        lens = [pick[draw(16)] for _ in range(1 + draw(9))] + [1 + draw(40)]
+        q, k, v, dout = inputs(lens, Hq, Hkv, D, dtype, token_major, seed=case)
+        cu = cu_of(lens)
+        out, lse = attention_varlen_fwd(q, k, v, cu, causal=causal)
+        done()
+        check_varlen_fwd(q, k, v, lens, out, lse, causal, D ** -0.5)
+        grads = attention_varlen_bwd(q, k, v, cu, out, lse, dout, causal=causal)
+        done()
+        check_varlen_bwd(q, k, v, lens, out, lse, dout, grads, causal, D ** -0.5)
