@@ -256,6 +256,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(bl.drain), 1);
     fence_mbar_init();
   }
+  if constexpr (VAR) {
+    if (warp == 3) var_acquire(p.var, vt, 4);
+  }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
@@ -279,16 +282,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nprod = min(kProducers, stages);
     const int pi = (warp == 0) ? 0 : warp - 1;
     if (lane == 0 && pi < nprod) {
-      if constexpr (VAR) {
-        var_map_acquire(m_q);
-        var_map_acquire(m_k);
-        var_map_acquire(m_v);
-        var_map_acquire(m_do);
+      if constexpr (!VAR) {
+        tma_prefetch_desc(m_q);
+        tma_prefetch_desc(m_k);
+        tma_prefetch_desc(m_v);
+        tma_prefetch_desc(m_do);
       }
-      tma_prefetch_desc(m_q);
-      tma_prefetch_desc(m_k);
-      tma_prefetch_desc(m_v);
-      tma_prefetch_desc(m_do);
       if (pi == 0 && n_res > 0) {
         mbar_expect_tx(bar(bl.a_full), n_res * s_n * kChunkBytes);
         for (int c = 0; c < s_n; ++c) {

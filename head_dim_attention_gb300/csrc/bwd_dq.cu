@@ -204,6 +204,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(bl.drain_b), 1);
     fence_mbar_init();
   }
+  if constexpr (VAR) {
+    if (warp == 3) var_acquire(p.var, vt, 5);
+  }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish_pair();
@@ -224,16 +227,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int S = is_a ? SA : SB;
     const int full0 = is_a ? bl.full_a : bl.full_b, empty0 = is_a ? bl.empty_a : bl.empty_b;
     const uint32_t ring = is_a ? ring_a : ring_b;
-    if constexpr (VAR) {
-      var_map_acquire(mB3);
-      var_map_acquire(is_a ? mB1 : mB2);
-      var_map_acquire(mA1);
-      var_map_acquire(mA2);
+    if constexpr (!VAR) {
+      tma_prefetch_desc(mB3);
+      tma_prefetch_desc(is_a ? mB1 : mB2);
     }
-    tma_prefetch_desc(mB3);
-    tma_prefetch_desc(is_a ? mB1 : mB2);
     if (is_a) {
-      tma_prefetch_desc(mA1);
+      if constexpr (!VAR) tma_prefetch_desc(mA1);
       if (rank == 0) mbar_expect_tx(bar(bl.res_full), 2 * res_bytes(NC));
       for (int c = 0; c < NC; ++c) {
         tma_load_4d_pair(a1_sm + c * kHalf, mA1, lead(bl.res_full), c * kChunk, g.s_row0, g.h, g.b);

@@ -311,6 +311,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kNrecv; ++i) mbar_expect_tx(bar((is_b ? bl.pt_full : bl.ds_full) + i), kTileX);
     fence_mbar_init();
   }
+  if constexpr (VAR) {
+    if (warp == 3) var_acquire(p.var, vt, 4);
+  }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish_pair();
@@ -330,12 +333,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int full0 = is_x ? bl.full_x : bl.full_g, empty0 = is_x ? bl.empty_x : bl.empty_g;
     const uint32_t ring = is_x ? ring_x : ring_g;
     if (is_x) {
-      if constexpr (VAR) {
-        var_map_acquire(mRes);
-        var_map_acquire(mX);
+      if constexpr (!VAR) {
+        tma_prefetch_desc(mRes);
+        tma_prefetch_desc(mX);
       }
-      tma_prefetch_desc(mRes);
-      tma_prefetch_desc(mX);
       if (pr == 0) mbar_expect_tx(bar(bl.res_full), 2 * G::kRes);
       for (int c = 4; c < NC; ++c)
         tma_load_4d_pair(res_sm + (c - 4) * kHalf, mRes, lead(bl.res_full), c * kChunk, g.s_row0, g.hs, g.b);
@@ -344,13 +345,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the stationary tile's chunks 0..3 (this CTA's 64 rows) on their way to TMEM,
         // through the staging tiles, idle until the first P or dS
         static_assert(4 * kHalf <= kNstage * kTileX, "four chunks fit the staging tiles");
-        var_map_acquire(mRes);
         mbar_expect_tx(bar(bl.st_full), 4 * kHalf);
         for (int c = 0; c < 4; ++c)
           tma_load_4d(stage_sm + c * kHalf, mRes, bar(bl.st_full), c * kChunk, g.s_row0, g.hs, g.b);
-        var_map_acquire(mG);
+      } else {
+        tma_prefetch_desc(mG);
       }
-      tma_prefetch_desc(mG);
     }
     bool ok = true;
     uint32_t it = 0;

@@ -264,6 +264,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     lo_flag[1] = 0;
     fence_mbar_init();
   }
+  if constexpr (VAR) {
+    if (warp == 3) var_acquire(p.var, vt, 3);
+  }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish_pair();
@@ -284,26 +287,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ring = is_k ? ring_k : ring_v;
     const uint32_t S = is_k ? kKSlots : G::kVSlots;
     if (is_k) {
-      if constexpr (VAR) {
-        var_map_acquire(m_qh);
-        var_map_acquire(m_kh);
+      if constexpr (!VAR) {
+        tma_prefetch_desc(m_qh);
+        tma_prefetch_desc(m_kh);
       }
-      tma_prefetch_desc(m_qh);
-      tma_prefetch_desc(m_kh);
       if (rank == 0) mbar_expect_tx(bar(bl.q_full), 2 * kQBytes);
       for (int c = kQtc; c < NC; ++c)
         tma_load_4d_pair(q_sm + (c - kQtc) * kHalfBytes, m_qh, lead(bl.q_full), c * kChunk,
                          q0 + 64 * static_cast<int>(rank), h, b);
     } else {
       if constexpr (VAR) {
-        var_map_acquire(m_qh);
         // Q's first kQtc chunks of this CTA's 64 rows, for the softmax warps (below)
         mbar_expect_tx(bar(bl.q_stage), kQtc * kHalfBytes);
         for (int c = 0; c < kQtc; ++c)
           tma_load_4d(p_sm + c * kHalfBytes, m_qh, bar(bl.q_stage), c * kChunk, q0 + 64 * static_cast<int>(rank), h, b);
-        var_map_acquire(m_v);
+      } else {
+        tma_prefetch_desc(m_v);
       }
-      tma_prefetch_desc(m_v);
     }
     bool ok = true;
     uint32_t it = 0;

@@ -146,6 +146,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     lo_flag[1] = 0;
     fence_mbar_init();
   }
+  if constexpr (VAR) {
+    if (warp == 3) var_acquire(p.var, vt, 3);
+  }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
@@ -168,14 +171,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nprod = min(kProducers, stages);
     const int pi = (warp == 0) ? 0 : warp - 1;
     if (lane == 0 && pi < nprod) {
-      if constexpr (VAR) {
-        var_map_acquire(m_q);
-        var_map_acquire(m_k);
-        var_map_acquire(m_v);
+      if constexpr (!VAR) {
+        tma_prefetch_desc(m_q);
+        tma_prefetch_desc(m_k);
+        tma_prefetch_desc(m_v);
       }
-      tma_prefetch_desc(m_q);
-      tma_prefetch_desc(m_k);
-      tma_prefetch_desc(m_v);
       if (pi == 0) {
         mbar_expect_tx(bar(bl.q_full), n * kChunkBytes);
         for (int c = 0; c < n; ++c) tma_load_4d(q_sm + c * kChunkBytes, m_q, bar(bl.q_full), c * kChunk, q0, h, b);

@@ -226,6 +226,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < kNbuf; ++i) mbar_expect_tx(bar(bl.rfull + i), kMsgBytes);
     fence_mbar_init();
   }
+  if constexpr (VAR) {
+    if (warp == 3) var_acquire(p.var, vt, 3);
+  }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish_pair();
@@ -241,12 +244,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // This CTA's slot s is free once the pair's MMAs reading it completed (the
     // first CTA's commit arrives here); the bytes of both CTAs are counted on
     // the first CTA's full[s].
-    if constexpr (VAR) {
-      var_map_acquire(m_qh);
-      var_map_acquire(m_kh);
+    if constexpr (!VAR) {
+      tma_prefetch_desc(m_qh);
+      tma_prefetch_desc(m_kh);
     }
-    tma_prefetch_desc(m_qh);
-    tma_prefetch_desc(m_kh);
     if (pr == 0) mbar_expect_tx(bar(bl.q_full), 2 * G::kQBytes);
     for (int c = kQtc; c < NC; ++c)
       tma_load_4d_pair(q_sm + (c - kQtc) * kHalfBytes, m_qh, lead(bl.q_full), c * kChunk,
@@ -274,8 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ pair B: the V ring
     // one slot per O block and key tile: this CTA's half of the block's
     // columns (one or two 64-column chunks) over the tile's 128 keys
-    if constexpr (VAR) var_map_acquire(m_v);
-    tma_prefetch_desc(m_v);
+    if constexpr (!VAR) tma_prefetch_desc(m_v);
     bool ok = true;
     uint32_t it = 0;
     for (int n = 0; n < kNblk * ntiles && ok; ++n) {

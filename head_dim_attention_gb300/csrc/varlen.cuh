@@ -50,9 +50,16 @@ __device__ __forceinline__ const CUtensorMap* var_map(const VarParams& v, const 
   return v.maps + static_cast<int64_t>(t.seq) * kVarMaps + which;
 }
 
-// Before a thread's first use of a map that the plan kernel wrote.
-__device__ __forceinline__ void var_map_acquire(const CUtensorMap* m) {
-  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+// One warp, ahead of the block's first barrier and so of its first TMA load: makes the
+// sequence's first `n` maps, which the plan kernel wrote, visible to this block's loads
+// (a map per lane).  No load that uses a map may be in flight meanwhile, and a map in
+// global memory takes no prefetch.tensormap, which is for the param and const spaces.
+__device__ __forceinline__ void var_acquire(const VarParams& v, const VarTile& t, int n) {
+  const int lane = threadIdx.x & 31;
+  if (lane < n)
+    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(
+                     reinterpret_cast<uint64_t>(var_map(v, t, lane)))
+                 : "memory");
 }
 
 __device__ __forceinline__ void* var_rows(const void* base, int64_t rows, int64_t row_stride) {
