@@ -195,6 +195,19 @@ def test_many_requests():
     run_tree(lens, [min(n, 1) for n in lens], 1, 2, 1, 64, 16, BF, seed=4)
 
 
+def test_requests_may_share_pages():
+    # three requests on one request's pages: all of them, a prefix that ends inside a page, one token
+    gen, host = torch.Generator(device="cuda").manual_seed(9), torch.Generator().manual_seed(9)
+    kc, vc, table, dk, dv = paged(gen, host, [200], 2, 32, 256, BF)
+    lens, drafts = [200, 150, 1], [2, 1, 1]
+    q = torch.randn(3, 4, 2, 256, generator=gen, device="cuda").to(BF)
+    out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:3], 7.0, device="cuda")
+    attention_tree_fwd(q, kc, vc, table.repeat(3, 1), i32(lens), draft_lens=i32(drafts), out=out, lse=lse)
+    done()
+    check_tree(q, [dk[0][:n] for n in lens], [dv[0][:n] for n in lens], lens, drafts, None, out, lse, 256 ** -0.5,
+               untouched=7.0)
+
+
 def test_mask_that_leaves_nothing():
     mask = torch.zeros(1, 3, 3, dtype=torch.bool, device="cuda")
     mask[0, 1, 0] = True  # row 1 sees draft 0, rows 0 and 2 see no draft
