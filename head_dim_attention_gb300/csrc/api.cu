@@ -561,16 +561,17 @@ void fill_plan(VarPlan* plan, VarParams* var, const VarLayout& l, const Common& 
   plan->status = status;
 }
 
-// Adds map `m` of `t` (box_rows rows to a box) to the plan.
-int plan_map(VarPlan* plan, const CUtensorMap& m, const ffpa_tensor_t* t, int box_rows) {
+// Adds a map of `t` (box_rows rows to a box) to the plan.
+int plan_map(VarPlan* plan, const ffpa_tensor_t* t, int box_rows) {
   int64_t st[3];
   tma_strides(t, st);
   const int i = plan->n_maps++;
-  plan->maps[i] = plan->short_maps[i] = m;
   plan->base[i] = t->data;
   plan->row_stride[i] = st[0];
   plan->short_rows[i] = varlen_short_rows(t->shape[3], t->shape[2], t->shape[1], st[0], st[1]);
-  return plan->short_rows[i] ? encode_map(&plan->short_maps[i], t, box_rows, 1) : FFPA_OK;
+  if (plan->short_rows[i] == t->shape[2]) plan->short_rows[i] = 0;  // all rows are as short: one form serves
+  const int rc = encode_map(&plan->maps[i], t, box_rows);
+  return rc || !plan->short_rows[i] ? rc : encode_map(&plan->short_maps[i], t, box_rows, 1);
 }
 
 int fwd_varlen_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_tensor_t* v, const int32_t* cu_seqlens,
@@ -588,14 +589,10 @@ int fwd_varlen_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_t
   if (!status) return FFPA_ERR_CUDA;
   FwdParams p;
   fill_fwd(&p, c, q, nullptr, causal, scale, out, lse, status);
-  FwdMaps m;
-  if ((rc = encode_fwd_maps(&m, q, k, v))) return rc;
-  VarPlan plan;
-  plan.n_maps = 0;
-  const bool pair = c.D >= 320;  // the CTA-pair kernels load halves of the Q and K tiles
-  const int half = pair ? kTileRows / 2 : kTileRows;
-  if ((rc = plan_map(&plan, pair ? m.q_half : m.q, q, half)) || (rc = plan_map(&plan, pair ? m.k_half : m.k, k, half)) ||
-      (rc = plan_map(&plan, m.v, v, kTileRows)))
+  const FwdMaps m = {};  // a packed call's kernels use the plan's maps
+  VarPlan plan = {};
+  const int half = c.D >= 320 ? kTileRows / 2 : kTileRows;  // the CTA-pair kernels load halves of the Q and K tiles
+  if ((rc = plan_map(&plan, q, half)) || (rc = plan_map(&plan, k, half)) || (rc = plan_map(&plan, v, kTileRows)))
     return rc;
   const VarLayout l = var_layout(c.Nq, n_seqs);
   timing_begin();
@@ -630,16 +627,12 @@ int bwd_varlen_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_t
   if (!status) return FFPA_ERR_CUDA;
   BwdParams p;
   fill_bwd(&p, c, q, k, v, nullptr, causal, scale, out, lse, dout, dq, dk, dv, status);
-  BwdMaps m;
-  if ((rc = encode_bwd_maps(&m, q, k, v, dout))) return rc;
-  VarPlan plan;
-  plan.n_maps = 0;
+  const BwdMaps m = {};
+  VarPlan plan = {};
   const bool pair = c.D >= 320;
   const int half = pair ? kTileRows / 2 : kTileRows;
-  if ((rc = plan_map(&plan, pair ? m.q_half : m.q, q, half)) || (rc = plan_map(&plan, pair ? m.k_half : m.k, k, half)) ||
-      (rc = plan_map(&plan, pair ? m.v_half : m.v, v, half)) ||
-      (rc = plan_map(&plan, pair ? m.dout_half : m.dout, dout, half)) ||
-      (pair && (rc = plan_map(&plan, m.k, k, kTileRows))))
+  if ((rc = plan_map(&plan, q, half)) || (rc = plan_map(&plan, k, half)) || (rc = plan_map(&plan, v, half)) ||
+      (rc = plan_map(&plan, dout, half)) || (pair && (rc = plan_map(&plan, k, kTileRows))))
     return rc;
   const VarLayout l = var_layout(c.Nq, n_seqs);
   const size_t rows = static_cast<size_t>(c.Hq) * c.Nq;
