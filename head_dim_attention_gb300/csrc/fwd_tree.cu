@@ -191,8 +191,9 @@ __host__ __device__ constexpr Bars bar_layout() {
               2 * kMaxSlots + 6, 2 * kMaxSlots + 7, 2 * kMaxSlots + 8, 2 * kMaxSlots + 9};
 }
 
+constexpr int kStats = 12 * 32;  // floats of one copy of the exchanged statistics: 12 softmax warps at most
 constexpr int kMiscBytes = 256 /* barriers, TMEM base, start */ + 128 /* work sums */ + 3 * 128 * 4 /* vis */ +
-                           96 * 8 * 2 /* rows in out and lse */ + 12 * 32 * 4 * 2 /* statistics */;
+                           96 * 8 * 2 /* rows in out and lse */ + kStats * 4 * 3 /* statistics, twice; one warp's own */;
 static_assert(kMiscBytes % 128 == 0, "tile alignment");
 __host__ __device__ constexpr int q_bytes(int n_chunks, int N) { return n_chunks * N * 128; }
 __host__ __device__ constexpr int fixed_bytes(int n_chunks, int N, bool bf16) {
@@ -337,8 +338,8 @@ __global__ void __launch_bounds__(tree_threads<N>(), tree_residency<N>())
   uint32_t* vis = reinterpret_cast<uint32_t*>(misc + 256 + 128);       // [3][128] draft -> rows that see it, C rows each
   int64_t* row_off = reinterpret_cast<int64_t*>(vis + 3 * 128);        // [N] offset of the row in out (0: padding)
   int64_t* row_lse = row_off + 96;                                     // [N] index of the row in lse
-  float* stat = reinterpret_cast<float*>(row_lse + 96);                // [warps][32] exchanged statistics
-  float* bcast = stat + 12 * 32;                                       // [warps][32] per-row values of one warp
+  float* stat = reinterpret_cast<float*>(row_lse + 96);                // [2][warps][32] exchanged statistics
+  float* bcast = stat + 2 * kStats;                                    // [warps][32] per-row values of one warp
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   static_assert(bl.count * 8 + 4 <= 176 && 176 + sizeof(Walk<N>) <= 252, "barrier area");
 
@@ -647,19 +648,23 @@ __global__ void __launch_bounds__(tree_threads<N>(), tree_residency<N>())
           for (int x = 0; x < C; ++x)
             if (!((see >> x) & 1u)) s[x] = -INFINITY;
         }
-        // row maxima: over the warp's 32 keys, then over the four warps
+        // row maxima: over the warp's 32 keys, then over the four warps.  Tiles take the
+        // two copies in turn: a warp that writes a copy again has passed the barrier of the
+        // tile between, where every warp arrives after it has read the copy.
+        const int at = (tc & 1) * kStats;
         {
           float mx[C];
 #pragma unroll
           for (int x = 0; x < C; ++x) mx[x] = s[x];
-          my_stat[lane] = reduce_columns<C>(mx, lane, MaxOp()) * p.scale_log2;
+          my_stat[at + lane] = reduce_columns<C>(mx, lane, MaxOp()) * p.scale_log2;
         }
         // A warp that gave up on a wait keeps taking part in the barriers: all
         // softmax warps leave together at the next unit.
         ok = bar_and(nb, 128, ok);
         float alpha = 1.f;
         {
-          const float m_tile = fmaxf(fmaxf(wg_stat[lane], wg_stat[32 + lane]), fmaxf(wg_stat[64 + lane], wg_stat[96 + lane]));
+          const float* x = wg_stat + at + lane;
+          const float m_tile = fmaxf(fmaxf(x[0], x[32]), fmaxf(x[64], x[96]));
           if (m_used == -INFINITY) {
             m_used = m_tile - kTop<BF16>;
           } else if (m_tile - kTop<BF16> > m_used + kRescaleLog2) {
@@ -729,7 +734,7 @@ __global__ void __launch_bounds__(tree_threads<N>(), tree_residency<N>())
       if (more) issue_q(after);
       if (ok) ok = mbar_wait<false>(bar(bl.pv_done), (tc - 1) & 1, status);
       ok = __all_sync(0xffffffffu, ok);
-      my_stat[lane] = reduce_columns<C>(l, lane, SumOp());
+      my_stat[lane] = reduce_columns<C>(l, lane, SumOp());  // pv_done: every warp has read the last tile's maxima
       ok = bar_and(nb, 128, ok);
       if (more) finish_q();
       const float sum = (wg_stat[lane] + wg_stat[32 + lane]) + (wg_stat[64 + lane] + wg_stat[96 + lane]);
