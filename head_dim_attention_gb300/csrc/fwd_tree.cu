@@ -36,7 +36,7 @@
 // about 2^-16.  At N = 96 the residual's 24 KB are worth more as a third ring
 // slot, and fp16 weights, rounded to 2^-11, need none.
 //
-// Warps: 0 and 2 TMA producers (alternate ring slots; the lanes of a warp issue
+// Warps: 0 and 2 TMA producers (even and odd ring slots; the lanes of a warp issue
 // a slot's boxes), 1 TMEM owner and MMA issuer, from 4 on softmax, correction
 // and epilogue: a warpgroup per 32 rows, 16 at N = 16 and 48 (thread = key of S^T,
 // then column of O^T).  Every wait is bounded.
@@ -413,8 +413,10 @@ __global__ void __launch_bounds__(tree_threads<N>(), tree_residency<N>())
   if (any && (warp == 0 || warp == 2)) {
     // ------------------------------------------------------------ TMA producers
     // Loads in the order of use: K of tile 0; then K of tile t + 1, V of tile t.
-    // Warp 0 takes the even loads, warp 2 the odd ones (two slots at least, so
-    // neither runs a round ahead of a slot's barrier).
+    // Warp 0 takes the loads of the even slots, warp 2 those of the odd ones.  A parity
+    // wait tells apart a barrier's current phase and the one before, and the releases of
+    // different slots may land in any order, so every load of a slot is the same warp's:
+    // it has then waited for each of the slot's releases.
     const int pi = warp >> 1;
     const int box = min(p.page, kTileRows), pieces = kTileRows / box;
     bool ok = true;
@@ -433,8 +435,8 @@ __global__ void __launch_bounds__(tree_threads<N>(), tree_residency<N>())
         row = pos % p.page + min(0, w.r.n - pos - box);  // the last box ends at the last valid row
       }
       for (int s2 = 0; s2 < kslots && ok; ++s2, ++it) {
-        if (static_cast<int>(it & 1) != pi) continue;
         const uint32_t s = it % slots, rd = it / slots;
+        if (static_cast<int>(s & 1) != pi) continue;
         ok = mbar_wait<false>(bar(bl.empty + s), (rd & 1) ^ 1, status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -454,12 +456,12 @@ __global__ void __launch_bounds__(tree_threads<N>(), tree_residency<N>())
         load_tile(&map_v, w, t);
       }
     } while (ok && w.next(p));
-    // the last release of every slot this warp loaded last (commit arrivals are
-    // not ordered with one another and must not land after the block is gone)
+    // the last release of each of this warp's slots (commit arrivals are not
+    // ordered with one another and must not land after the block is gone)
     if (lane == 0)
-      for (uint32_t s = 0; s < static_cast<uint32_t>(slots) && s < it && ok; ++s) {
-        const uint32_t last = s + ((it - 1 - s) / slots) * slots;
-        if (static_cast<int>(last & 1) == pi) mbar_wait<false>(bar(bl.empty + s), (last / slots) & 1, status);
+      for (uint32_t s = pi; s < static_cast<uint32_t>(slots) && s < it && ok; s += 2) {
+        const uint32_t rounds = (it - 1 - s) / slots;  // full ones before the slot's last load
+        mbar_wait<false>(bar(bl.empty + s), rounds & 1, status);
       }
   } else if (any && warp == 1 && lane == 0) {
     // ------------------------------------------------------------ MMA issuer

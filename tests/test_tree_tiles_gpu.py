@@ -64,3 +64,19 @@ def many_tiles(lens, T, Hq, D, page, dtype, runs, busy):
 def test_row_maxima_from_tile_to_tile(T, Hq, D, dtype):
     lens = [1500 - 7 * i for i in range(80)]  # 12 key tiles each, about 6 to a block
     many_tiles(lens, T, Hq, D, 64, dtype, runs=12, busy=True)
+
+
+@pytest.mark.parametrize("T,Hq,D,dtype", [
+    (1, 4, 64, FP),     # five slots
+    (1, 4, 128, FP),    # three, two blocks to an SM
+    (24, 2, 256, BF),   # five
+    (12, 8, 384, BF),   # three
+    (8, 8, 512, BF),
+    (12, 8, 512, BF),
+    (8, 8, 704, FP),
+    (1, 8, 832, FP),    # five
+    (6, 8, 1024, BF),   # three
+])
+def test_rings_of_an_odd_number_of_slots(T, Hq, D, dtype):
+    lens = [2300 - 31 * i for i in range(40)]  # 18 key tiles and fewer, whole rings many times over
+    many_tiles(lens, T, Hq, D, 32, dtype, runs=3, busy=False)
