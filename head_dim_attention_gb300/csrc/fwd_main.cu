@@ -161,16 +161,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0 || warp == 2 || warp == 3) {
     // ------------------------------------------------------------ TMA producers
     // Three warps (one lane each) issue the ring loads: producer pi owns every
-    // nprod-th load of the sequence and waits only for its own slot to be
-    // released. Arming a barrier and issuing a TMA load blocks the issuing
-    // thread for ~500 cycles, so one thread alone cannot keep the ring full.
+    // third slot and waits only for its own slots to be released. Arming a
+    // barrier and issuing a TMA load blocks the issuing thread for ~500 cycles,
+    // so one thread alone cannot keep the ring full.
     // A parity wait tells apart only the current and the previous phase of a
-    // barrier, so no producer may run two rounds ahead of a slot's barrier:
-    // producer pi waits for load i - stages before issuing load i, having
-    // issued load i - nprod, which needs nprod <= stages.
-    const int nprod = min(kProducers, stages);
+    // barrier, and releases of different slots may land in any order, so every
+    // load of a slot is the same producer's: it has then waited for each of
+    // the slot's releases. (Dealt out load by load, five slots passed from
+    // producer to producer, and one could find a slot two rounds behind.)
     const int pi = (warp == 0) ? 0 : warp - 1;
-    if (lane == 0 && pi < nprod) {
+    if (lane == 0 && pi < stages) {
       if constexpr (!VAR) {
         tma_prefetch_desc(m_q);
         tma_prefetch_desc(m_k);
@@ -187,8 +187,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // costs the SM a few hundred cycles whatever its size, so two 16 KB tiles
       // per phase move nearly twice the bytes of one.
       auto load = [&](const CUtensorMap* m, int c0, int cn, int row) {
-        if (ok && static_cast<int>(it % nprod) == pi) {
-          const uint32_t s = it % stages, r = it / stages;
+        const uint32_t s = it % stages, r = it / stages;
+        if (ok && static_cast<int>(s % kProducers) == pi) {
           ok = mbar_wait(bar(bl.empty + s), (r & 1) ^ 1, status);
           if (ok) {
             mbar_expect_tx(bar(bl.full + s), cn * kChunkBytes);
@@ -206,14 +206,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j >= 1)
           for (int c = 0; c < n; c += G) load(m_v, c, min(G, n - c), (j - 1) * kTileRows);
       }
-      // Drain: wait for the last release of each ring slot whose last load was
-      // ours. The MMA warp's commit arrives on empty[s] only when the MMAs
-      // reading the slot are done, and commit arrivals are not ordered with
-      // respect to one another, so one still in flight at exit would land in
-      // the next CTA's shared memory.
-      for (uint32_t s = 0; s < static_cast<uint32_t>(stages) && s < it; ++s) {
-        const uint32_t last = s + ((it - 1 - s) / stages) * stages;
-        if (static_cast<int>(last % nprod) == pi) mbar_wait(bar(bl.empty + s), (last / stages) & 1, status);
+      // Drain: wait for the last release of each of our ring slots. The MMA
+      // warp's commit arrives on empty[s] only when the MMAs reading the slot
+      // are done, and commit arrivals are not ordered with respect to one
+      // another, so one still in flight at exit would land in the next CTA's
+      // shared memory.
+      for (uint32_t s = pi; s < static_cast<uint32_t>(stages) && s < it; s += kProducers) {
+        const uint32_t rounds = (it - 1 - s) / stages;  // full ones before the slot's last load
+        mbar_wait(bar(bl.empty + s), rounds & 1, status);
       }
       if (pi == 0) mbar_wait(bar(bl.q_full), 0, status);
     }
