@@ -15,7 +15,30 @@ namespace ffpa {
 // Per-device status word, set by kernels whose bounded waits expire.
 __device__ uint32_t g_status_word;
 
+namespace {
+// A first call on a device creates the scratch pool, looks up the status word and
+// loads kernels: none of it touches a stream, but a thread that captures one in
+// the default mode may not do it.  While this lives, it may, so a first call can
+// be a captured one.
+struct CaptureGuard {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  CaptureGuard() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~CaptureGuard() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
+// A host thread's first call may be its first use of CUDA at all: the runtime then
+// has no current context for it yet, and the driver's map encoder, which every
+// tensor-core path calls before any kernel, fails.  A free of nothing makes it current.
+void bind_thread() {
+  thread_local bool bound = false;
+  if (bound) return;
+  CaptureGuard guard;
+  bound = cudaFree(nullptr) == cudaSuccess;
+}
+}  // namespace
+
 uint32_t* device_status_word() {
+  bind_thread();
   static std::mutex mu;
   static uint32_t* cache[64] = {};
   int dev = 0;
@@ -506,16 +529,6 @@ int bwd_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_tensor_t
   cudaError_t e2 = cudaFreeAsync(scratch, st);
   return cuda_rc(e != cudaSuccess ? e : e2);
 }
-
-// A first call on a device creates the scratch pool, looks up the status word and
-// loads kernels: none of it touches a stream, but a thread that captures one in
-// the default mode may not do it.  While this lives, it may, so a first call can
-// be a captured one.
-struct CaptureGuard {
-  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
-  CaptureGuard() { cudaThreadExchangeStreamCaptureMode(&mode); }
-  ~CaptureGuard() { cudaThreadExchangeStreamCaptureMode(&mode); }
-};
 
 // ------------------------------------------------------------ packed sequences
 // Checks beyond check_common: one batch, as many keys as queries, and the starts.
