@@ -756,14 +756,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int MODE, bool BF16>
 cudaError_t launch_mode(const BwdParams& p_in, const BwdMaps& m, cudaStream_t st) {
   BwdParams p = p_in;
-  constexpr int kMaxSmem = 232448;
   // Keep as many stationary operands resident as leave a ring of >= 3 stages
   // (>= 2 when nothing is resident).
   int n_res = (MODE == kDV) ? 1 : 2;
   int room = 0;
   for (; n_res >= 0; --n_res) {
     const Plan base = make_plan(p.n_chunks, 0, n_res, 1);
-    room = kMaxSmem - 1024 - base.total;
+    room = kMaxBlockSmem - 1024 - base.total;
     if (room / kChunkBytes >= 3) break;
   }
   if (n_res < 0) n_res = 0;
@@ -777,7 +776,7 @@ cudaError_t launch_mode(const BwdParams& p_in, const BwdMaps& m, cudaStream_t st
   const Plan plan = make_plan(p.n_chunks, stages, n_res, G);
   const int smem = plan.total + 1024;
   auto kern = p.var.tiles ? bwd_main_kernel<MODE, BF16, true> : bwd_main_kernel<MODE, BF16, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBlockSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   const int slots = p.var.tiles ? p.var.slots : (MODE == kDQ ? p.q_tiles : p.kv_tiles);

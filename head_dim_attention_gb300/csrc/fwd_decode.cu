@@ -723,7 +723,7 @@ template <int R, int G, int U, bool BF16>
 cudaError_t launch_stream(const DecodeParams& p, cudaStream_t st) {
   const size_t smem = (static_cast<size_t>(8) * R * p.D + 16 * R) * 4;
   auto k1 = decode_stream_kernel<R, G, U, BF16>;
-  cudaError_t e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBlockSmem);
   if (e != cudaSuccess) return e;
   k1<<<dim3(p.n_splits, p.Hq / p.heads_per_cta, p.B), kDecThreads, smem, st>>>(p);
   return cudaSuccess;
@@ -735,7 +735,7 @@ cudaError_t launch_bulk(const DecodeParams& p, cudaStream_t st) {
   const size_t merge = (static_cast<size_t>(8) * R * p.D + 16 * R) * 4;
   const size_t smem = (ring > merge ? ring : merge) + 2 * kBulkStages * 8;
   auto k1 = decode_bulk_kernel<R, G, BF16>;
-  cudaError_t e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBlockSmem);
   if (e != cudaSuccess) return e;
   k1<<<dim3(p.n_splits, p.Hq / p.heads_per_cta, p.B), kDecThreads, smem, st>>>(p);
   return cudaSuccess;
@@ -767,7 +767,7 @@ cudaError_t launch_decode_impl(const DecodeParams& p, cudaStream_t st) {
     if (p.heads_per_cta != 1) return cudaErrorInvalidValue;
     const size_t smem = (static_cast<size_t>(p.Nq) * p.D + static_cast<size_t>(p.Nq) * p.split_len + 2 * p.Nq) * 4;
     auto k1 = decode_split_kernel<BF16>;
-    e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBlockSmem);
     if (e != cudaSuccess) return e;
     k1<<<dim3(p.n_splits, p.Hq, p.B), kDecThreads, smem, st>>>(p);
   }

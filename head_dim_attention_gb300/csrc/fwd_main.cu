@@ -523,9 +523,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <bool BF16>
 cudaError_t launch_impl(const FwdParams& p_in, const FwdMaps& m, cudaStream_t st) {
   FwdParams p = p_in;
-  constexpr int kMaxSmem = 232448;  // 227 KB opt-in per block
   const SmemPlan base = smem_plan(p.n_chunks, 0, 1);
-  const int room = kMaxSmem - 1024 - base.total;
+  const int room = kMaxBlockSmem - 1024 - base.total;
   // Two chunk tiles per ring slot when at least two such slots fit, else one.
   int G = (room / (2 * kChunkBytes) >= 2) ? 2 : 1;
   int stages = room / (G * kChunkBytes);
@@ -536,7 +535,7 @@ cudaError_t launch_impl(const FwdParams& p_in, const FwdMaps& m, cudaStream_t st
   const SmemPlan plan = smem_plan(p.n_chunks, stages, G);
   const int smem = plan.total + 1024;  // + alignment slack
   auto kern = p.var.tiles ? fwd_main_kernel<BF16, true> : fwd_main_kernel<BF16, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBlockSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.var.tiles ? p.var.slots : p.q_tiles, p.Hq, p.B);

@@ -54,7 +54,6 @@ namespace {
 constexpr int p_bytes(int N) { return 2 * N * 128; }
 constexpr bool keeps_residual(int N, bool bf16) { return bf16 && N <= 64; }
 constexpr int kMaxSlots = 6;
-constexpr int kMaxSmem = 232448;
 constexpr float kRescaleLog2 = 8.0f;  // rescale O only when a row's max grows by > 2^8
 // The largest weight of a row is 2^kTop when its reference is set: fp16 ends at
 // 2^16 above and, in steps of 2^-24, below, so its weights are moved up by 2^6
@@ -1019,7 +1018,7 @@ template <int N, bool BF16>
 cudaError_t launch_n(const TreeParams& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
   const int smem = fixed_bytes(p.n_chunks, N, BF16) + p.slots * p.slot_bytes;
   auto kern = tree_kernel<N, BF16>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBlockSmem);
   if (e != cudaSuccess) return e;
   timing_mark(st);
   kern<<<p.blocks, tree_threads<N>(), smem, st>>>(mk, mv, p);
@@ -1063,7 +1062,7 @@ int tree_shape(TreeParams* p, int64_t rows, bool bf16) {
   const int fixed = fixed_bytes(p->n_chunks, n, bf16);
   const bool two = p->D <= 256 && n <= 32;
   // an SM has 228 KB, of which a block's own 1 KB is reserved for the system
-  const int room = two ? (233472 - 2 * 1024) / 2 : kMaxSmem;
+  const int room = two ? (233472 - 2 * 1024) / 2 : kMaxBlockSmem;
   p->slots = std::min(kMaxSlots, (room - fixed) / p->slot_bytes);
   p->tmem_cols = two ? 256 : 512;
   return two ? 2 : 1;

@@ -18,6 +18,10 @@ enum : uint32_t {
 constexpr int kTileRows = 128;  // query/key rows per tile (the MMA M)
 constexpr int kChunk = 64;      // D columns per chunk (one 128-byte swizzled row)
 constexpr int kChunkBytes = kTileRows * kChunk * 2;  // 16 KB
+// Dynamic shared memory a block may opt in to (227 KB).  The opt-in is a property of the
+// kernel, shared by all host threads: a kernel whose need varies from call to call always
+// opts in to this much, so that one call never lowers what another is about to launch with.
+constexpr int kMaxBlockSmem = 232448;
 
 // Packed sequences (varlen.cuh).
 constexpr int kVarMaps = 5;  // TMA maps per sequence, at most

@@ -1,4 +1,10 @@
-"""Host threads that call the library through its C entry points."""
+"""Host threads that call the library through its C entry points, which run without the
+interpreter's lock: a thread's first use of CUDA, and two threads at once with head
+dimensions that share a kernel.
+
+A kernel's shared memory differs from head dimension to head dimension; one
+thread's call may not change what another's launch is allowed.
+"""
 import threading
 
 import pytest
@@ -8,6 +14,7 @@ from head_dim_attention_gb300 import _lib, ffpa_check_status
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
+CALLS = 1500
 
 
 def tree_call(lib, D):
@@ -69,3 +76,39 @@ def test_first_use_of_cuda_in_a_thread(lib, make):
     torch.cuda.synchronize()
     assert codes == [0] and ffpa_check_status() == 0
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.parametrize("make,small,large", [
+    (tree_call, dict(D=64), dict(D=512)),
+    (forward_call, dict(D=64), dict(D=256)),
+    (forward_call, dict(D=64, rows=1, keys=300), dict(D=512, rows=1, keys=300)),
+    (forward_call, dict(D=64, rows=1, keys=300, spread=True), dict(D=512, rows=1, keys=300, spread=True)),
+    (forward_call, dict(D=64, rows=5, keys=300), dict(D=1024, rows=16, keys=300)),
+    (backward_call, dict(D=64), dict(D=256)),
+], ids=["tree", "forward", "decode", "decode, spread rows", "decode, many rows", "backward"])
+def test_two_threads_with_different_head_dimensions(lib, make, small, large):
+    calls = [make(lib, **small), make(lib, **large)]
+    want = []
+    for _, outs, call in calls:
+        assert call(None) == 0
+        torch.cuda.synchronize()
+        want.append([x.clone() for x in outs])
+    streams = [torch.cuda.Stream() for _ in calls]
+    codes, gate = [[], []], threading.Barrier(2)
+
+    def work(i):
+        _, _, call = calls[i]
+        gate.wait()
+        for _ in range(CALLS):
+            codes[i].append(call(streams[i].cuda_stream))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert [sum(c != 0 for c in x) for x in codes] == [0, 0]
+    assert ffpa_check_status() == 0
+    for (_, outs, _), expect in zip(calls, want):
+        assert all(torch.equal(a, b) for a, b in zip(outs, expect))
