@@ -119,15 +119,16 @@ void tma_strides(const ffpa_tensor_t* t, int64_t out[3]) {
   out[2] = sb;
 }
 
-// The map of the tensor's first `rows` rows (0: all of them).
-int encode_map(CUtensorMap* m, const ffpa_tensor_t* t, int box_rows = kTileRows, int64_t rows = 0) {
+// `packed`: of a packed call, with the second batch of kVarOuterStride.
+int encode_map(CUtensorMap* m, const ffpa_tensor_t* t, int box_rows = kTileRows, bool packed = false) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return FFPA_ERR_CUDA;
   int64_t st[3];
   tma_strides(t, st);
-  const cuuint64_t dims[4] = {(cuuint64_t)t->shape[3], (cuuint64_t)(rows ? rows : t->shape[2]),
-                              (cuuint64_t)t->shape[1], (cuuint64_t)t->shape[0]};
-  const cuuint64_t strides[3] = {(cuuint64_t)st[0] * 2, (cuuint64_t)st[1] * 2, (cuuint64_t)st[2] * 2};
+  const cuuint64_t dims[4] = {(cuuint64_t)t->shape[3], (cuuint64_t)t->shape[2], (cuuint64_t)t->shape[1],
+                              packed ? 2 : (cuuint64_t)t->shape[0]};
+  const cuuint64_t strides[3] = {(cuuint64_t)st[0] * 2, (cuuint64_t)st[1] * 2,
+                                 packed ? kVarOuterStride : (cuuint64_t)st[2] * 2};
   const cuuint32_t box[4] = {(cuuint32_t)kChunk, (cuuint32_t)box_rows, 1, 1};
   const cuuint32_t es[4] = {1, 1, 1, 1};
   const CUtensorMapDataType dt =
@@ -581,10 +582,7 @@ int plan_map(VarPlan* plan, const ffpa_tensor_t* t, int box_rows) {
   const int i = plan->n_maps++;
   plan->base[i] = t->data;
   plan->row_stride[i] = st[0];
-  plan->short_rows[i] = varlen_short_rows(t->shape[3], t->shape[2], t->shape[1], st[0], st[1]);
-  if (plan->short_rows[i] == t->shape[2]) plan->short_rows[i] = 0;  // all rows are as short: one form serves
-  const int rc = encode_map(&plan->maps[i], t, box_rows);
-  return rc || !plan->short_rows[i] ? rc : encode_map(&plan->short_maps[i], t, box_rows, 1);
+  return encode_map(&plan->maps[i], t, box_rows, true);
 }
 
 int fwd_varlen_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_tensor_t* v, const int32_t* cu_seqlens,

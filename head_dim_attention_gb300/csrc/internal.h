@@ -25,6 +25,13 @@ constexpr int kMaxBlockSmem = 232448;
 
 // Packed sequences (varlen.cuh).
 constexpr int kVarMaps = 5;  // TMA maps per sequence, at most
+// Their maps have a second batch this many bytes behind the first, which no load names.
+// The plan makes a sequence's map from that of all rows by tensormap.replace (base and
+// row count), and what the encoder makes of a tensor may depend on more than the fields
+// replaced: on how far its elements lie apart, say.  With this stride, past the memory of
+// the GPU and below the encoder's limit of 2^40, a tensor of one row lies as far apart as
+// one of a million, and the replaced map is the one that the encoder makes of the sequence.
+constexpr uint64_t kVarOuterStride = 1ull << 39;
 struct VarParams {
   const int4* tiles;        // [slots] (sequence or -1, tile, first row, length); nullptr: not a packed call
   const CUtensorMap* maps;  // [sequences][kVarMaps]
@@ -32,11 +39,9 @@ struct VarParams {
   int total;                // rows of q, k and v: the head stride of lse, delta and lse2
 };
 struct VarPlan {
-  CUtensorMap maps[kVarMaps];        // of the whole packed tensors
-  CUtensorMap short_maps[kVarMaps];  // of their first rows: sequences of at most short_rows start from these
+  CUtensorMap maps[kVarMaps];    // of the whole packed tensors (kVarOuterStride)
   const void* base[kVarMaps];    // their data pointers
   int64_t row_stride[kVarMaps];  // elements
-  int short_rows[kVarMaps];
   int n_maps;
   const int32_t* cu;             // [n_seqs + 1] first rows, ascending
   int n_seqs, total, slots, causal;
@@ -227,8 +232,6 @@ inline void set_overlap(cudaLaunchAttribute* attr) {
 }
 // Fills the tile slots and the per-sequence maps of a packed call (varlen.cu).
 cudaError_t launch_varlen_plan(const VarPlan& p, cudaStream_t s);
-// Rows of the longest sequence whose maps are made from short_maps (0: none); row and head strides in elements.
-int varlen_short_rows(int64_t D, int64_t rows, int64_t heads, int64_t row_stride, int64_t head_stride);
 
 cudaError_t launch_fwd_main(const FwdParams& p, const FwdMaps& m, bool bf16, cudaStream_t s);
 // Full-D CTA-pair forward (fwd_fulld.cu): D = 512, one pair holds all of O.

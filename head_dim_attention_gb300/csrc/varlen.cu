@@ -12,8 +12,6 @@
 // Starts that do not ascend within 0 .. T describe no sequence: such an entry
 // counts as length 0 and the status word reports it; no read or write follows
 // from it.
-#include <algorithm>
-
 #include "varlen.cuh"
 
 namespace ffpa {
@@ -48,8 +46,7 @@ __global__ void __launch_bounds__(kPlanThreads) varlen_plan_kernel(const __grid_
     const SeqRange r = seq_range(p, s);
     if (r.len == 0) return;  // no tile uses these maps
     const uint32_t sm = smem_u32(stage[warp]);
-    reinterpret_cast<uint32_t*>(stage[warp])[lane] = reinterpret_cast<const uint32_t*>(
-        r.len <= p.short_rows[which] ? &p.short_maps[which] : &p.maps[which])[lane];
+    reinterpret_cast<uint32_t*>(stage[warp])[lane] = reinterpret_cast<const uint32_t*>(&p.maps[which])[lane];
     __syncwarp();
     if (lane == 0) {
       const uint64_t base = reinterpret_cast<uint64_t>(p.base[which]) + 2ull * static_cast<uint64_t>(r.start) * p.row_stride[which];
@@ -128,20 +125,6 @@ __global__ void __launch_bounds__(kPlanThreads) varlen_plan_kernel(const __grid_
 }
 
 }  // namespace
-
-// cuTensorMapEncodeTiled gives a tensor whose elements span less than 128 KB a map that
-// differs from a larger one's in more than its sizes (over 200,000 random 4-D shapes the
-// span alone decided, at this value).  The map of a large tensor, shrunk to a short
-// sequence, is therefore not what the encoder makes of that sequence, and a random run of
-// small packed calls with such maps ended in an illegal address.  So the plan starts from
-// the map of all rows only for sequences that span as much, and for shorter ones from the
-// map of the first row: its maps are then the encoder's of each sequence, byte for byte.
-int varlen_short_rows(int64_t D, int64_t rows, int64_t heads, int64_t row_stride, int64_t head_stride) {
-  constexpr int64_t kSmallSpan = (128 << 10) / 2;  // elements
-  const int64_t room = kSmallSpan - 1 - D - (heads - 1) * head_stride;
-  if (room < 0) return 0;
-  return static_cast<int>(row_stride > 0 ? std::min(room / row_stride + 1, rows) : rows);
-}
 
 cudaError_t launch_varlen_plan(const VarPlan& p, cudaStream_t s) {
   const int64_t items = static_cast<int64_t>(p.n_seqs) * p.n_maps;

@@ -28,9 +28,8 @@ struct Tensor {
 static EncodeFn encode_fn;
 static CUtensorMap encode(const Tensor& t, int64_t first, int64_t rows) {
   CUtensorMap m;
-  const cuuint64_t dims[4] = {(cuuint64_t)t.D, (cuuint64_t)rows, (cuuint64_t)t.heads, 1};
-  const cuuint64_t strides[3] = {(cuuint64_t)t.row_stride * 2, (cuuint64_t)t.head_stride * 2,
-                                 (cuuint64_t)(t.head_stride * t.heads) * 2};
+  const cuuint64_t dims[4] = {(cuuint64_t)t.D, (cuuint64_t)rows, (cuuint64_t)t.heads, 2};
+  const cuuint64_t strides[3] = {(cuuint64_t)t.row_stride * 2, (cuuint64_t)t.head_stride * 2, kVarOuterStride};
   const cuuint32_t box[4] = {64, (cuuint32_t)t.box_rows, 1, 1}, one[4] = {1, 1, 1, 1};
   const CUresult r = encode_fn(&m, t.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                                t.base + 2 * first * t.row_stride, dims, strides, box, one,
@@ -66,7 +65,7 @@ int main() {
   std::mt19937 gen(7);
   auto draw = [&](int a, int b) { return std::uniform_int_distribution<int>(a, b)(gen); };
   const int edges[] = {63, 64, 65, 127, 128, 129, 255, 256, 257};
-  long maps = 0, small = 0, wrong_maps = 0, wrong_tiles = 0;
+  long maps = 0, wrong_maps = 0, wrong_tiles = 0;
   for (int call = 0; call < 2000; ++call) {
     const int n = call % 50 == 0 ? draw(500, 3000) : draw(1, 12);
     std::vector<int> lens(n), first(n + 1, 0);
@@ -86,11 +85,9 @@ int main() {
       const bool token_major = draw(0, 1);
       t[w] = Tensor{data + 512 * draw(0, 1000), D, heads, token_major ? heads * D : D, token_major ? D : T * D,
                     draw(0, 1) ? 64 : 128, draw(0, 1) == 1};
-      p.maps[w] = p.short_maps[w] = encode(t[w], 0, T);
+      p.maps[w] = encode(t[w], 0, T);
       p.base[w] = t[w].base;
       p.row_stride[w] = t[w].row_stride;
-      p.short_rows[w] = varlen_short_rows(D, T, heads, t[w].row_stride, t[w].head_stride);
-      if (p.short_rows[w]) p.short_maps[w] = encode(t[w], 0, 1);
     }
     p.cu = cu;
     p.n_seqs = n;
@@ -115,7 +112,6 @@ int main() {
       for (int w = 0; lens[s] && w < p.n_maps; ++w) {
         const CUtensorMap want = encode(t[w], first[s], lens[s]);
         ++maps;
-        small += lens[s] <= p.short_rows[w];
         if (std::memcmp(&want, &got[static_cast<size_t>(s) * kVarMaps + w], sizeof want) != 0 && wrong_maps++ < 5)
           std::printf("map differs: %d rows from %d of %lld, D %lld, %lld heads, strides %lld %lld\n", lens[s], first[s],
                       (long long)T, (long long)D, (long long)t[w].heads, (long long)t[w].row_stride,
@@ -140,7 +136,6 @@ int main() {
   }
   uint32_t word = 0;
   ok(cudaMemcpy(&word, status, sizeof word, cudaMemcpyDeviceToHost));
-  std::printf("%ld maps (%ld from the short form), %ld differ; %ld wrong tiles; status %u\n", maps, small, wrong_maps,
-              wrong_tiles, word);
-  return wrong_maps || wrong_tiles || word || !small || small == maps;
+  std::printf("%ld maps, %ld differ; %ld wrong tiles; status %u\n", maps, wrong_maps, wrong_tiles, word);
+  return wrong_maps || wrong_tiles || word || !maps;
 }
