@@ -640,11 +640,11 @@ int bwd_varlen_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_t
   fill_bwd(&p, c, q, k, v, nullptr, causal, scale, out, lse, dout, dq, dk, dv, status);
   const BwdMaps m = {};
   VarPlan plan = {};
-  const bool pair = c.D >= 320;
-  const int half = pair ? kTileRows / 2 : kTileRows;
+  const int half = c.D >= 320 ? kTileRows / 2 : kTileRows;
   if ((rc = plan_map(&plan, q, half)) || (rc = plan_map(&plan, k, half)) || (rc = plan_map(&plan, v, half)) ||
-      (rc = plan_map(&plan, dout, half)) || (pair && (rc = plan_map(&plan, k, kTileRows))))
+      (rc = plan_map(&plan, dout, half)))
     return rc;
+  if (bwd_dq_supported(p) && (rc = plan_map(&plan, k, kTileRows))) return rc;  // its gradient operand: whole K tiles
   const VarLayout l = var_layout(c.Nq, n_seqs);
   const size_t rows = static_cast<size_t>(c.Hq) * c.Nq;
   timing_begin();
