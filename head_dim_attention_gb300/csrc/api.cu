@@ -94,12 +94,13 @@ struct Shape4 {
 
 bool is_half_dtype(int dt) { return dt == FFPA_F16 || dt == FFPA_BF16; }
 
-// Validate one [B, H, N, D] half-precision tensor.
+// Validate one [B, H, N, D] half-precision tensor (with N = 0 its data may be null and its strides anything).
 int check_bhnd(const ffpa_tensor_t* t, int dtype, const Shape4& want) {
-  if (!t || !t->data || t->reserved != 0) return FFPA_ERR_INVALID_ARG;
+  if (!t || (!t->data && want.N > 0) || t->reserved != 0) return FFPA_ERR_INVALID_ARG;
   if (t->dtype != dtype) return is_half_dtype(t->dtype) ? FFPA_ERR_INVALID_ARG : FFPA_ERR_UNSUPPORTED;
   if (t->shape[0] != want.B || t->shape[1] != want.H || t->shape[2] != want.N || t->shape[3] != want.D)
     return FFPA_ERR_INVALID_ARG;
+  if (want.N == 0) return FFPA_OK;
   if (t->stride[3] != 1) return FFPA_ERR_UNSUPPORTED;
   if (reinterpret_cast<uintptr_t>(t->data) % 16 != 0) return FFPA_ERR_ALIGNMENT;
   for (int i = 0; i < 3; ++i) {
@@ -143,8 +144,9 @@ struct Common {
   int dtype;
 };
 
+// `least` rows of q and of k and v: 0 where a call without rows does nothing.
 int check_common(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_tensor_t* v,
-                 const ffpa_tensor_t* bias, float scale, Common* c) {
+                 const ffpa_tensor_t* bias, float scale, Common* c, int least = 1) {
   if (!q || !k || !v) return FFPA_ERR_INVALID_ARG;
   if (!is_half_dtype(q->dtype)) return FFPA_ERR_UNSUPPORTED;
   c->dtype = q->dtype;
@@ -154,7 +156,7 @@ int check_common(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_tens
   c->D = q->shape[3];
   c->Hkv = k->shape[1];
   c->Nkv = k->shape[2];
-  if (c->B < 1 || c->Hq < 1 || c->Hkv < 1 || c->Nq < 1 || c->Nkv < 1 || c->D < 1) return FFPA_ERR_INVALID_ARG;
+  if (c->B < 1 || c->Hq < 1 || c->Hkv < 1 || c->Nq < least || c->Nkv < least || c->D < 1) return FFPA_ERR_INVALID_ARG;
   if (c->B > 65535 || c->Hq > 65535 || c->Nq > (1ll << 30) || c->Nkv > (1ll << 30)) return FFPA_ERR_UNSUPPORTED;
   if (c->Hq % c->Hkv != 0) return FFPA_ERR_INVALID_ARG;
   if (c->D % 64 != 0 || c->D < 64 || c->D > 1024) return FFPA_ERR_UNSUPPORTED;
@@ -178,10 +180,11 @@ int check_common(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_tens
 }
 
 int check_lse(const ffpa_tensor_t* lse, const Common& c) {
-  if (!lse->data || lse->reserved != 0) return FFPA_ERR_INVALID_ARG;
+  if ((!lse->data && c.Nq > 0) || lse->reserved != 0) return FFPA_ERR_INVALID_ARG;
   if (lse->dtype != FFPA_F32) return FFPA_ERR_UNSUPPORTED;
   if (lse->shape[0] != c.B || lse->shape[1] != c.Hq || lse->shape[2] != c.Nq || lse->shape[3] != 1)
     return FFPA_ERR_INVALID_ARG;
+  if (c.Nq == 0) return FFPA_OK;
   // contiguous [B, Hq, Nq]
   if ((c.Nq > 1 && lse->stride[2] != 1) || (c.Hq > 1 && lse->stride[1] != c.Nq) ||
       (c.B > 1 && lse->stride[0] != c.Hq * c.Nq))
@@ -589,11 +592,12 @@ int fwd_varlen_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_t
                     int n_seqs, int causal, float scale, const ffpa_tensor_t* out, const ffpa_tensor_t* lse,
                     ffpa_stream_t stream) {
   Common c;
-  int rc = check_common(q, k, v, nullptr, scale, &c);
+  int rc = check_common(q, k, v, nullptr, scale, &c, 0);
   if (rc) return rc;
   if ((rc = check_packed(c, cu_seqlens, n_seqs, causal))) return rc;
   if ((rc = check_bhnd(out, c.dtype, {c.B, c.Hq, c.Nq, c.D}))) return rc;
   if (lse && (rc = check_lse(lse, c))) return rc;
+  if (c.Nq == 0) return FFPA_OK;  // no rows
   CaptureGuard guard;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint32_t* status = device_status_word();
@@ -622,7 +626,7 @@ int bwd_varlen_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_t
                     const ffpa_tensor_t* dout, const ffpa_tensor_t* dq, const ffpa_tensor_t* dk,
                     const ffpa_tensor_t* dv, ffpa_stream_t stream) {
   Common c;
-  int rc = check_common(q, k, v, nullptr, scale, &c);
+  int rc = check_common(q, k, v, nullptr, scale, &c, 0);
   if (rc) return rc;
   if ((rc = check_packed(c, cu_seqlens, n_seqs, causal))) return rc;
   if ((rc = check_bhnd(out, c.dtype, {c.B, c.Hq, c.Nq, c.D}))) return rc;
@@ -632,6 +636,7 @@ int bwd_varlen_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_t
   if ((rc = check_bhnd(dv, c.dtype, {c.B, c.Hkv, c.Nkv, c.D}))) return rc;
   if (!lse) return FFPA_ERR_INVALID_ARG;
   if ((rc = check_lse(lse, c))) return rc;
+  if (c.Nq == 0) return FFPA_OK;  // no rows
   CaptureGuard guard;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint32_t* status = device_status_word();
@@ -690,7 +695,7 @@ int fwd_tree_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* kc, const ffpa_te
   c.B = q->shape[0]; c.Hq = q->shape[1]; c.Nq = q->shape[2]; c.D = q->shape[3];
   c.Hkv = kc->shape[1];
   c.Nkv = 0;
-  if (c.B < 1 || c.Hq < 1 || c.Hkv < 1 || c.Nq < 1 || c.D < 1) return FFPA_ERR_INVALID_ARG;
+  if (c.B < 1 || c.Hq < 1 || c.Hkv < 1 || c.Nq < 0 || c.D < 1) return FFPA_ERR_INVALID_ARG;
   if (c.B > 65535 || c.Hq > 65535 || c.Nq > kMaxDrafts) return FFPA_ERR_UNSUPPORTED;
   if (c.Hq % c.Hkv != 0) return FFPA_ERR_INVALID_ARG;
   if (c.D % 64 != 0 || c.D < 64 || c.D > 1024) return FFPA_ERR_UNSUPPORTED;
@@ -704,6 +709,7 @@ int fwd_tree_impl(const ffpa_tensor_t* q, const ffpa_tensor_t* kc, const ffpa_te
     return rc;
   if (max_pages < 1 || (mask && mask_batch != 1 && mask_batch != c.B)) return FFPA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(max_pages) * kc->shape[2] > (1ll << 30)) return FFPA_ERR_UNSUPPORTED;
+  if (c.Nq == 0) return FFPA_OK;  // no drafts
   CaptureGuard guard;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint32_t* status = device_status_word();
@@ -792,12 +798,13 @@ int cache_append_impl(const ffpa_tensor_t* k, const ffpa_tensor_t* v, const ffpa
   if (!is_half_dtype(k->dtype)) return FFPA_ERR_UNSUPPORTED;
   const int64_t D = k->shape[3];
   const Shape4 want = {1, kc->shape[1], k->shape[2], D};
-  if (want.H < 1 || want.N < 1 || D < 1) return FFPA_ERR_INVALID_ARG;
+  if (want.H < 1 || want.N < 0 || D < 1) return FFPA_ERR_INVALID_ARG;
   if (D % 64 != 0 || D > 1024 || want.N > (1ll << 30)) return FFPA_ERR_UNSUPPORTED;
   int rc;
   if ((rc = check_bhnd(k, k->dtype, want)) || (rc = check_bhnd(v, k->dtype, want))) return rc;
   if ((rc = check_caches(kc, vc, k->dtype, D))) return rc;
-  if ((rc = check_ints(slots, 8, true))) return rc;
+  if ((rc = check_ints(slots, 8, want.N > 0))) return rc;
+  if (want.N == 0) return FFPA_OK;  // no rows
   AppendParams p = {};
   p.k = k->data;
   p.v = v->data;

@@ -166,7 +166,9 @@ int ffpa_bwd_dropout(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_
  *   causal            0 or 1: row i of a sequence sees its rows j <= i
  *
  * Strides are free as in ffpa_fwd, so token-major storage [T, H, D] is the
- * view with head stride D.  A sequence may be empty.  Rows outside every
+ * view with head stride D.  A sequence may be empty; so may the whole batch: with
+ * T = 0 the call is checked as any other (data pointers of tensors without rows may
+ * be null), launches nothing and does not read cu_seqlens.  Rows outside every
  * sequence (before cu_seqlens[0], behind the last one) are neither read into
  * a result nor written, and no value of one sequence, NaN included, reaches
  * another.  Within a sequence the contract of ffpa_fwd / ffpa_bwd holds: a
@@ -206,7 +208,8 @@ int ffpa_bwd_varlen(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_t
  *
  * ffpa_fwd_tree: attention of drafted tokens over the cache.
  *
- *   q, out      [B, Hq, T, D], T <= 128 (1: plain decoding), Hkv divides Hq
+ *   q, out      [B, Hq, T, D], T <= 128 (1: plain decoding; 0: nothing is done),
+ *               Hkv divides Hq
  *   max_pages   columns of block_table; max_pages * page <= 2^30
  *   seq_lens    device int32 [B]: tokens of the request in the cache, its
  *               drafted tokens included (they are the last ones)
@@ -262,7 +265,7 @@ int ffpa_cache_plan(const int32_t* lens, const int32_t* new_lens, int n_reqs, in
  * ffpa_cache_append: writes the rows of k and v [1, Hkv, T, D] to their slots:
  * row t goes to row slots[t] % page of page slots[t] / page.  slots is device
  * int64 [T], contiguous; a negative slot skips its row, one past the last page
- * is skipped and reported.  Slots that occur twice keep either row, possibly
+ * is skipped and reported.  With T = 0 nothing is done.  Slots that occur twice keep either row, possibly
  * mixed in pieces of 8 elements.
  */
 int ffpa_cache_append(const ffpa_tensor_t* k, const ffpa_tensor_t* v, const ffpa_tensor_t* k_cache,
