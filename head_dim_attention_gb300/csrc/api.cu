@@ -120,16 +120,16 @@ void tma_strides(const ffpa_tensor_t* t, int64_t out[3]) {
   out[2] = sb;
 }
 
-// `packed`: of a packed call, with the second batch of kVarOuterStride.
-int encode_map(CUtensorMap* m, const ffpa_tensor_t* t, int box_rows = kTileRows, bool packed = false) {
+// `row_only`: of its first head's first row, with the tensor's strides.
+int encode_map(CUtensorMap* m, const ffpa_tensor_t* t, int box_rows = kTileRows, bool row_only = false) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return FFPA_ERR_CUDA;
   int64_t st[3];
   tma_strides(t, st);
-  const cuuint64_t dims[4] = {(cuuint64_t)t->shape[3], (cuuint64_t)t->shape[2], (cuuint64_t)t->shape[1],
-                              packed ? 2 : (cuuint64_t)t->shape[0]};
-  const cuuint64_t strides[3] = {(cuuint64_t)st[0] * 2, (cuuint64_t)st[1] * 2,
-                                 packed ? kVarOuterStride : (cuuint64_t)st[2] * 2};
+  cuuint64_t dims[4] = {(cuuint64_t)t->shape[3], (cuuint64_t)t->shape[2], (cuuint64_t)t->shape[1],
+                        (cuuint64_t)t->shape[0]};
+  if (row_only) dims[1] = dims[2] = dims[3] = 1;
+  const cuuint64_t strides[3] = {(cuuint64_t)st[0] * 2, (cuuint64_t)st[1] * 2, (cuuint64_t)st[2] * 2};
   const cuuint32_t box[4] = {(cuuint32_t)kChunk, (cuuint32_t)box_rows, 1, 1};
   const cuuint32_t es[4] = {1, 1, 1, 1};
   const CUtensorMapDataType dt =
@@ -585,6 +585,7 @@ int plan_map(VarPlan* plan, const ffpa_tensor_t* t, int box_rows) {
   const int i = plan->n_maps++;
   plan->base[i] = t->data;
   plan->row_stride[i] = st[0];
+  plan->heads[i] = static_cast<int>(t->shape[1]);
   return encode_map(&plan->maps[i], t, box_rows, true);
 }
 

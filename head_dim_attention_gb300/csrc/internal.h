@@ -25,13 +25,6 @@ constexpr int kMaxBlockSmem = 232448;
 
 // Packed sequences (varlen.cuh).
 constexpr int kVarMaps = 5;  // TMA maps per sequence, at most
-// Their maps have a second batch this many bytes behind the first, which no load names.
-// The plan makes a sequence's map from that of all rows by tensormap.replace (base and
-// row count), and what the encoder makes of a tensor may depend on more than the fields
-// replaced: on how far its elements lie apart, say.  With this stride, past the memory of
-// the GPU and below the encoder's limit of 2^40, a tensor of one row lies as far apart as
-// one of a million, and the replaced map is the one that the encoder makes of the sequence.
-constexpr uint64_t kVarOuterStride = 1ull << 39;
 struct VarParams {
   const int4* tiles;        // [slots] (sequence or -1, tile, first row, length); nullptr: not a packed call
   const CUtensorMap* maps;  // [sequences][kVarMaps]
@@ -39,9 +32,10 @@ struct VarParams {
   int total;                // rows of q, k and v: the head stride of lse, delta and lse2
 };
 struct VarPlan {
-  CUtensorMap maps[kVarMaps];    // of the whole packed tensors (kVarOuterStride)
+  CUtensorMap maps[kVarMaps];    // of the first head's first row of the packed tensors
   const void* base[kVarMaps];    // their data pointers
   int64_t row_stride[kVarMaps];  // elements
+  int heads[kVarMaps];
   int n_maps;
   const int32_t* cu;             // [n_seqs + 1] first rows, ascending
   int n_seqs, total, slots, causal;

@@ -5,9 +5,16 @@
 // index t has t + 1 key tiles), with a counting sort over kBins work classes:
 // a histogram, a scan from the heaviest class down, and a scatter.  The order
 // inside a class is whatever the shared-memory atomics give; it decides only
-// when a tile runs, never what it computes.  The other blocks copy the maps,
-// one warp per (sequence, map): 128 bytes through shared memory, two fields
+// when a tile runs, never what it computes.  The other blocks make the maps,
+// one warp per (sequence, map): 128 bytes through shared memory, three fields
 // replaced, published with the tensormap release that var_acquire pairs with.
+//
+// The maps start from that of a single row (base, rows and heads are replaced) and
+// not from that of all rows, because the encoder gives large tensors another form
+// than small ones, and a map of that form over few rows faults: kernels that
+// loaded short sequences through such maps ended in an illegal address twice, once
+// in about three hundred small calls.  The form of the smallest tensor holds for
+// every size: it is what a map gets that is encoded before its sizes are known.
 //
 // Starts that do not ascend within 0 .. T describe no sequence: such an entry
 // counts as length 0 and the status word reports it; no read or write follows
@@ -52,6 +59,7 @@ __global__ void __launch_bounds__(kPlanThreads) varlen_plan_kernel(const __grid_
       const uint64_t base = reinterpret_cast<uint64_t>(p.base[which]) + 2ull * static_cast<uint64_t>(r.start) * p.row_stride[which];
       asm volatile("tensormap.replace.tile.global_address.shared::cta.b1024.b64 [%0], %1;" ::"r"(sm), "l"(base) : "memory");
       asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(sm), "r"(r.len) : "memory");
+      asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 2, %1;" ::"r"(sm), "r"(p.heads[which]) : "memory");
     }
     __syncwarp();
     const CUtensorMap* dst = p.out_maps + static_cast<int64_t>(s) * kVarMaps + which;

@@ -2,9 +2,9 @@
 // and v are several sequences one after the other.
 //
 // A sequence is treated as a tensor of its own.  Every TMA map a kernel uses is
-// copied once per sequence with its base moved to the sequence's first row and
-// its row count set to the sequence's length (tensormap.replace, in the plan
-// kernel of varlen.cu), so rows of a neighbour are out of range: they arrive as
+// made once per sequence, with the sequence's first row as its base and its
+// length as the row count (tensormap.replace, in the plan kernel of varlen.cu),
+// so rows of a neighbour are out of range: they arrive as
 // zeros, exactly as rows past the end of an unpacked tensor do, and neither a
 // value nor a NaN of one sequence can reach another.  With pointers moved and
 // Nq = Nkv = length (localize below) the kernels' index arithmetic is that of
