@@ -177,9 +177,10 @@ int ffpa_bwd_dropout(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_
  *
  * cu_seqlens is read on the device, so a captured call follows new lengths at
  * every replay.  The entries must ascend within 0 .. T.  A pair that does not
- * describes no sequence: its rows are not written, and ffpa_check_status
- * returns FFPA_ERR_INVALID_ARG.  Ranges that overlap are not detected; their
- * shared rows then hold either result.
+ * describes no sequence: it writes no rows, and ffpa_check_status returns
+ * FFPA_ERR_INVALID_ARG.  Where the starts descend like that, the ranges of the
+ * pairs after it can overlap those before; the rows they share then hold either
+ * result or are left.
  *
  * Two launches (forward: the plan, the attention kernel) or five (backward,
  * D >= 320: four): the plan gives every block its sequence and tile.  Its
@@ -226,6 +227,16 @@ int ffpa_bwd_varlen(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_t
  * Nothing behind a request's length is read, so unused rows of its last page
  * may hold anything; the values of drafts that a mask hides must be finite.
  * A missing page (number out of range) counts as zeros.
+ *
+ * T > 128 is FFPA_ERR_UNSUPPORTED, and the packed calls attend to the rows of the
+ * batch alone: a chunk of more than 128 new tokens behind cached ones can be
+ * planned and written, but its attention has to be asked for in pieces of 128 (a
+ * piece's tokens being the last of seq_lens, and written before the call).
+ *
+ * The weights of the sum over V are 16-bit operands.  fp16: rounded once, 2^-11 of
+ * a weight.  bf16: a rounded weight and its rounding residual, 2^-16, for up to 64
+ * rows per kv head and launch tile; the 96-row tiles (D <= 512 and more than 64
+ * rows, group x drafts, whenever 96 make fewer tiles) round once, 2^-8.
  * Two launches; fp32 partials of at most 2 n D floats per block (n rows, 16 to
  * 96; one block per SM, two for D <= 256) in stream-ordered scratch.
  */
