@@ -994,8 +994,7 @@ __global__ void selftest_wait_kernel(uint32_t* status) {
 extern "C" int ffpa_selftest_wait_timeout(ffpa_stream_t stream) {
   uint32_t* status = device_status_word();
   if (!status) return FFPA_ERR_CUDA;
-  selftest_wait_kernel<<<1, 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(status);
-  return cudaGetLastError() == cudaSuccess ? FFPA_OK : FFPA_ERR_CUDA;
+  return cuda_rc(launch_kernel(selftest_wait_kernel, dim3(1), 32, 0, reinterpret_cast<cudaStream_t>(stream), status));
 }
 
 extern "C" int ffpa_version(void) { return 200; }

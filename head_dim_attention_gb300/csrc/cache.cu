@@ -179,8 +179,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __gr
 
 cudaError_t launch_cache_plan(const PlanParams& p, cudaStream_t s) {
   const bool one = p.max_new <= 4 * kPlanThreads;
-  cache_plan_kernel<<<1, kPlanThreads, 0, s>>>(p, one ? 1 : 0);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_kernel(cache_plan_kernel, dim3(1), kPlanThreads, 0, s, p, one ? 1 : 0);
   if (e != cudaSuccess || one) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((p.max_new + 255) / 256), 1, 1);
@@ -195,8 +194,8 @@ cudaError_t launch_cache_plan(const PlanParams& p, cudaStream_t s) {
 cudaError_t launch_cache_append(const AppendParams& p, int sms, cudaStream_t s) {
   const int64_t items = p.T * p.H * (p.D / 8);
   const int64_t blocks = (items + kAppendThreads - 1) / kAppendThreads;
-  cache_append_kernel<<<static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(sms) * 32)), kAppendThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(sms) * 32)));
+  return launch_kernel(cache_append_kernel, grid, kAppendThreads, 0, s, p);
 }
 
 }  // namespace ffpa

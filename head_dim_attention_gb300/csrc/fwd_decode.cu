@@ -725,8 +725,7 @@ cudaError_t launch_stream(const DecodeParams& p, cudaStream_t st) {
   auto k1 = decode_stream_kernel<R, G, U, BF16>;
   cudaError_t e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBlockSmem);
   if (e != cudaSuccess) return e;
-  k1<<<dim3(p.n_splits, p.Hq / p.heads_per_cta, p.B), kDecThreads, smem, st>>>(p);
-  return cudaSuccess;
+  return launch_kernel(k1, dim3(p.n_splits, p.Hq / p.heads_per_cta, p.B), kDecThreads, smem, st, p);
 }
 
 template <int R, int G, bool BF16>
@@ -737,8 +736,7 @@ cudaError_t launch_bulk(const DecodeParams& p, cudaStream_t st) {
   auto k1 = decode_bulk_kernel<R, G, BF16>;
   cudaError_t e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBlockSmem);
   if (e != cudaSuccess) return e;
-  k1<<<dim3(p.n_splits, p.Hq / p.heads_per_cta, p.B), kDecThreads, smem, st>>>(p);
-  return cudaSuccess;
+  return launch_kernel(k1, dim3(p.n_splits, p.Hq / p.heads_per_cta, p.B), kDecThreads, smem, st, p);
 }
 
 template <bool BF16>
@@ -769,12 +767,10 @@ cudaError_t launch_decode_impl(const DecodeParams& p, cudaStream_t st) {
     auto k1 = decode_split_kernel<BF16>;
     e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBlockSmem);
     if (e != cudaSuccess) return e;
-    k1<<<dim3(p.n_splits, p.Hq, p.B), kDecThreads, smem, st>>>(p);
+    e = launch_kernel(k1, dim3(p.n_splits, p.Hq, p.B), kDecThreads, smem, st, p);
   }
   if (e != cudaSuccess) return e;
   timing_mark(st);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   return launch_combine<BF16>(p, st);
 }
 
@@ -794,7 +790,7 @@ cudaError_t launch_combine(const DecodeParams& p, cudaStream_t st) {
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, decode_combine_kernel<BF16>, p);
   timing_mark(st);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return e;
 }
 
 }  // namespace

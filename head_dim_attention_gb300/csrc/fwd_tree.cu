@@ -1021,9 +1021,9 @@ cudaError_t launch_n(const TreeParams& p, const CUtensorMap& mk, const CUtensorM
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBlockSmem);
   if (e != cudaSuccess) return e;
   timing_mark(st);
-  kern<<<p.blocks, tree_threads<N>(), smem, st>>>(mk, mv, p);
+  e = launch_kernel(kern, dim3(p.blocks), tree_threads<N>(), smem, st, mk, mv, p);
   timing_mark(st);
-  if ((e = cudaGetLastError()) != cudaSuccess || p.blocks < 2) return e;
+  if (e != cudaSuccess || p.blocks < 2) return e;
   e = launch_merge<N, BF16>(p, st);
   timing_mark(st);
   return e;

@@ -219,6 +219,19 @@ struct BwdMaps {
 
 bool dtype_is_bf16(int dtype);
 
+// Launches a kernel and returns this launch's own error.  (After a <<<>>> launch the
+// error has to be asked of cudaGetLastError, which also returns what an earlier call
+// that failed has left there.)
+template <class... Params, class... Args>
+inline cudaError_t launch_kernel(void (*kern)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                                 const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
 // Launch attribute of a kernel that may start before the one ahead of it in the stream has ended (varlen.cuh).
 inline void set_overlap(cudaLaunchAttribute* attr) {
   attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -137,8 +137,7 @@ __global__ void __launch_bounds__(kPlanThreads) varlen_plan_kernel(const __grid_
 cudaError_t launch_varlen_plan(const VarPlan& p, cudaStream_t s) {
   const int64_t items = static_cast<int64_t>(p.n_seqs) * p.n_maps;
   const unsigned blocks = 1 + static_cast<unsigned>((items + kPlanThreads / 32 - 1) / (kPlanThreads / 32));
-  varlen_plan_kernel<<<blocks, kPlanThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_kernel(varlen_plan_kernel, dim3(blocks), kPlanThreads, 0, s, p);
 }
 
 }  // namespace ffpa
