@@ -989,10 +989,14 @@ cudaError_t launch_merge_q(const TreeParams& p, cudaStream_t st) {
 }
 
 // Few units (fewer than a quarter of the blocks: five pieces or more on average)
-// take the deep form, as long as its blocks are two waves or so.  One request of
-// 131,072 keys, 8 heads on one kv head, D = 512 (152 pieces): 88 us in the wide form,
-// 58 in the deep one; 12 requests of 96 rows on two kv heads (19 pieces, 9216 deep
-// blocks): 126 and 155.
+// take the deep form, as long as its blocks are two waves or so.  Whole calls, wide /
+// deep, with as many keys in all (us; * what the rule takes):
+//   rows x units     1 x 1      1 x 32     8 x 1     8 x 16     8 x 37     48 x 4     48 x 8
+//   D = 64         82 / 21*   25 / 24*   83 / 21*  26 / 24*   31 / 30*   47 / 38*   42 / 38*
+//   D = 512        96 / 56*   93 / 93*   97 / 57*  97 / 97*  109 / 113* 113 / 104* 106* / 108
+//   D = 1024      151 / 96*   97 / 96*  153 / 97* 100 / 102*  99* / 109 123* / 113 114* / 123
+// and with 90 rows, 4 and 16 units: 50 / 41* and 45* / 49 (D = 64), 117* / 110 and
+// 108* / 136 (D = 512).  Where the rule errs it costs 9% at most.
 template <int N, bool BF16>
 cudaError_t launch_merge(const TreeParams& p, cudaStream_t st) {
   const int64_t units = static_cast<int64_t>(p.B) * p.Hkv * ((static_cast<int64_t>(p.group) * p.T + N - 1) / N);
