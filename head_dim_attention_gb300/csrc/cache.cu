@@ -182,7 +182,8 @@ cudaError_t launch_cache_plan(const PlanParams& p, cudaStream_t s) {
   // tokens 5.1 to 6.2 us and 6.4 to 7.7 (1 to 512 requests), at 2048 6.1 to 8.8 and 6.5
   // to 8.8, at 4096 7.2 to 10.4 and 6.7 to 9.1, at 16384 14 to 25 and 7.8 to 11.6.
   const bool one = p.max_new <= 2 * kPlanThreads;
-  const cudaError_t e = launch_kernel(cache_plan_kernel, dim3(1), kPlanThreads, 0, s, p, one ? 1 : 0);
+  cudaError_t e = launch_kernel(cache_plan_kernel, dim3(1), kPlanThreads, 0, s, p, one ? 1 : 0);
+  timing_mark(s);
   if (e != cudaSuccess || one) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((p.max_new + 255) / 256), 1, 1);
@@ -191,7 +192,9 @@ cudaError_t launch_cache_plan(const PlanParams& p, cudaStream_t s) {
   cudaLaunchAttribute attr[1];
   cfg.attrs = attr;
   set_overlap(&attr[cfg.numAttrs++]);
-  return cudaLaunchKernelEx(&cfg, cache_slots_kernel, p);
+  e = cudaLaunchKernelEx(&cfg, cache_slots_kernel, p);
+  timing_mark(s);
+  return e;
 }
 
 cudaError_t launch_cache_append(const AppendParams& p, int sms, cudaStream_t s) {

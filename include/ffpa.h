@@ -330,13 +330,16 @@ int ffpa_check_status(ffpa_stream_t stream);
  *   events  array of `count` cudaEvent_t handles created by the caller, or NULL
  *   count   0 disables the hook
  *
- * While set (per calling host thread), every later ffpa_fwd / ffpa_bwd call on
- * this thread records events[0] on its stream before its first kernel launch
- * and events[i] right after its i-th launch, for as many events as given
- * (ffpa_fwd launches 1 kernel on the fused path and 2 on the decode and
- * key-split paths; ffpa_bwd launches 4 for D <= 256 and 3 above).  The caller keeps ownership of
- * the events.  Returns FFPA_ERR_INVALID_ARG if count < 0, count > 8, or
- * events (or one of its first `count` handles) is NULL with count > 0.
+ * While set (per calling host thread), every later call of this thread records
+ * events[0] on its stream before its first kernel launch and events[i] right
+ * after its i-th launch, for as many events as given (ffpa_fwd launches 1 kernel
+ * on the fused path and 2 on the decode and key-split paths; ffpa_bwd launches 4
+ * for D <= 256 and 3 above; the packed calls one more, the plan; ffpa_fwd_tree 2,
+ * or 1 where one block takes all of it; ffpa_cache_plan 1, or 2 for many tokens;
+ * ffpa_cache_append 1).  Events between the launches of a packed or paged call
+ * keep these from overlapping.  The caller keeps ownership of the events.  Returns
+ * FFPA_ERR_INVALID_ARG if count < 0, count > 8, or events (or one of its first
+ * `count` handles) is NULL with count > 0.
  */
 int ffpa_set_timing_events(void* const* events, int count);
 
