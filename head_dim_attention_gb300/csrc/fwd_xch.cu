@@ -464,7 +464,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_l1(bias_row + min(kv0 + 32, p.Nkv - 1));
         prefetch_l1(bias_row + min(kv0 + 63, p.Nkv - 1));
       }
-      const bool got = __all_sync(0xffffffffu, mbar_wait<false>(bar(bl.s_full + (j & 1)), (j >> 1) & 1, status));
+      const bool got =
+          ok && __all_sync(0xffffffffu, mbar_wait<false>(bar(bl.s_full + (j & 1)), (j >> 1) & 1, status));
       float s[64];
       if (got) {
         tc_fence_after();
@@ -584,8 +585,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ok = fr;
       }
+      // a warp that gave up here still meets the other warp of its rows at the next
+      // tile's barrier, and both leave together there
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      if (!ok) break;
     }
     if (lane == 0) bulk_wait_read<0>();
     // pair B's last commits to each buffer's rfree land here before exit
