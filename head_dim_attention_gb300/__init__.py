@@ -91,8 +91,8 @@ def attention_bwd(q, k, v, out, lse, dout, bias=None, causal=False, scale=None, 
 def attention_varlen_fwd(q, k, v, cu_seqlens, causal=False, scale=None, out=None, lse=None, stream=None):
     """O and lse of self-attention over packed sequences: q [1,Hq,T,D], k/v [1,Hkv,T,D] (any strides; a
     token-major [T,H,D] tensor x is x.transpose(0, 1)[None]), sequence s in rows cu_seqlens[s] ..
-    cu_seqlens[s+1]-1 (int32, on the device).  Rows outside the sequences are left as they are (unset where
-    out/lse are allocated here)."""
+    cu_seqlens[s+1]-1 (int32, on the device); T = 0 does nothing.  Rows outside the sequences are left as they
+    are (unset where out/lse are allocated here)."""
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
     if out is None:
@@ -123,7 +123,8 @@ def attention_tree_fwd(q, k_cache, v_cache, block_table, seq_lens, draft_lens=No
     seq_lens [B] counts a request's tokens in the cache, its drafts (the last
     draft_lens[b] of them, T each if not given) included.  A draft sees every
     token before the drafts and the drafts its row of tree_mask (bool [B or 1,
-    T, T]) marks, without one those up to itself.  T = 1 is plain decoding.
+    T, T]) marks, without one those up to itself.  T = 1 is plain decoding, T <=
+    128: a longer chunk of new tokens takes a call for each 128 of them.
     Rows past a request's drafts are left as they are (unset where out/lse are
     allocated here)."""
     if scale is None:
