@@ -182,6 +182,11 @@ int ffpa_bwd_dropout(const ffpa_tensor_t* q, const ffpa_tensor_t* k, const ffpa_
  * pairs after it can overlap those before; the rows they share then hold either
  * result or are left.
  *
+ * The backward's P and dS are 16-bit operands, as in ffpa_bwd: each is rounded once
+ * (fp16 2^-11, bf16 2^-8 of a value), and for D >= 320 dS is formed from the rounded
+ * P, so dK lies about 1.7 times as far from the exact gradient as one that is
+ * computed in fp32 and rounded at the end.
+ *
  * Two launches (forward: the plan, the attention kernel) or five (backward,
  * D >= 320: four): the plan gives every block its sequence and tile.  Its
  * scratch, (640 n_seqs + 16 slots) bytes for at most (T + 127 n_seqs) / 128
